@@ -19,6 +19,7 @@ CSA2_OK = 0
 STATUS_NAMES = {0: "CSA2_OK", 1: "CSA2_ERR_INVALID_ARG", 2: "CSA2_ERR_UNSUPPORTED_SHAPE", 3: "CSA2_ERR_CUDA",
                 4: "CSA2_ERR_DEVICE_CHECK", 5: "CSA2_ERR_WORKSPACE"}
 DEV_INDEX_RANGE, DEV_TIMEOUT, DEV_APPEND_RANGE, DEV_BAD_POSITION = 0x1, 0x2, 0x4, 0x8
+DEV_NO_PAGE, DEV_BAD_SEQUENCE = 0x10, 0x20
 
 
 class Csa2Error(RuntimeError):
@@ -39,8 +40,16 @@ class SwaCacheDesc(ctypes.Structure):
                 ("W_cap", ctypes.c_int32), ("D", ctypes.c_int32), ("window", ctypes.c_int32)]
 
 
+class PagePoolDesc(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("n_entries", ctypes.c_void_p), ("n_pages", ctypes.c_int32),
+                ("page", ctypes.c_int32), ("n_seq", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("m", ctypes.c_int32)]
+
+
 _P, _I, _I64, _SZ, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 _PM, _PS = ctypes.POINTER(MainCacheDesc), ctypes.POINTER(SwaCacheDesc)
+_PP = ctypes.POINTER(PagePoolDesc)
 
 SIGNATURES = {
     "csa2_append_quant": (_I, [_PM, _P, _P, _P, _PS, _P, _P, _I, _P]),
@@ -59,6 +68,14 @@ SIGNATURES = {
     "csa2_topk_noalloc": (_I, [_P, _I, _I64, _I, _P, _P, _I, _P, _I, _P, _P]),
     "csa2_sparse_attn_decode": (_I, [_PM, _PS, _P, _P, _I, _I, _P, _I, _F, _P, _P, _SZ, _P]),
     "csa2_attn_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "csa2_pages_append": (_I, [_PP, _PM, _P, _P, _P, _P, _SZ, _P]),
+    "csa2_pages_workspace_size": (_SZ, [_PP, _I]),
+    "csa2_pages_fork": (_I, [_PP, _P, _P, _I, _P, _SZ, _P]),
+    "csa2_pages_compact": (_I, [_PP, _P, _P, _SZ, _P]),
+    "csa2_prefix_attn_decode": (_I, [_PP, _P, _I, _PS, _P, _P, _I, _I, _I, _F, _P, _P, _SZ, _P]),
+    "csa2_prefix_attn_workspace_size": (_SZ, [_I, _I, _I, _I]),
+    "csa2_window_attn": (_I, [_PS, _PS, _P, _P, _I, _I, _F, _P, _P, _SZ, _P]),
+    "csa2_window_attn_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "csa2_debug_inject_timeout": (None, [ctypes.c_uint32]),
     "csa2_last_error": (ctypes.c_char_p, []),
     "csa2_device_status": (_I, [_P, ctypes.POINTER(ctypes.c_uint32), _I]),
@@ -175,6 +192,16 @@ class SwaCache:
         self.B, self.W_cap, self.D, self.scale, self.window = B, W_cap, D, float(scale), window
         self.rows = torch.zeros(B, W_cap, D, dtype=torch.uint8, device=device)
 
+    @classmethod
+    def of(cls, rows, scale=1.0, window=128):
+        """A cache over rows [B][W_cap][D] that exist already."""
+        if rows.dim() != 3 or rows.dtype != torch.uint8 or not rows.is_contiguous():
+            raise ValueError("rows must be a contiguous uint8 tensor [B][W_cap][D]")
+        c = cls.__new__(cls)
+        c.B, c.W_cap, c.D = rows.shape
+        c.scale, c.window, c.rows = float(scale), int(window), rows
+        return c
+
     def __setattr__(self, name, value):   # any change rebuilds the descriptor
         object.__setattr__(self, name, value)
         object.__setattr__(self, "_desc", None)
@@ -184,6 +211,50 @@ class SwaCache:
         if self._desc is None:
             object.__setattr__(self, "_desc", SwaCacheDesc(self.rows.data_ptr(), self.scale, self.B, self.W_cap,
                                                            self.D, self.window))
+        return self._desc
+
+
+class PagePool:
+    """Device tensors of a paged FP4 cache (layout of csa2_page_pool), empty."""
+
+    def __init__(self, n_pages, page, n_seq, max_pages, D, m=1, device="cuda"):
+        self._set(torch.zeros(n_pages, page, D // 2, dtype=torch.uint8, device=device),
+                  torch.zeros(n_pages, page, D // 16, dtype=torch.uint8, device=device),
+                  torch.zeros(n_pages, dtype=torch.int32, device=device),
+                  torch.full((n_seq, max_pages), -1, dtype=torch.int32, device=device),
+                  torch.zeros(n_seq, dtype=torch.int32, device=device), m)
+
+    @classmethod
+    def of(cls, codes, scales, refs, table, n_entries, m=1):
+        """A pool over tensors that exist already."""
+        c = cls.__new__(cls)
+        c._set(codes, scales, refs, table, n_entries, m)
+        return c
+
+    def _set(self, codes, scales, refs, table, n_entries, m):
+        n_pages, page, half = codes.shape
+        D = 2 * half
+        n_seq, max_pages = table.shape
+        for t, dtype, shape in ((codes, torch.uint8, (n_pages, page, half)),
+                                (scales, torch.uint8, (n_pages, page, D // 16)),
+                                (refs, torch.int32, (n_pages,)), (table, torch.int32, (n_seq, max_pages)),
+                                (n_entries, torch.int32, (n_seq,))):
+            if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != codes.device:
+                raise ValueError(f"page pool planes: expected contiguous {dtype} {shape} on {codes.device}, got "
+                                 f"{t.dtype} {tuple(t.shape)} on {t.device}")
+        self.codes, self.scales, self.refs, self.table, self.n_entries = codes, scales, refs, table, n_entries
+        self.n_pages, self.page, self.n_seq, self.max_pages, self.D, self.m = n_pages, page, n_seq, max_pages, D, m
+
+    def __setattr__(self, name, value):   # any change rebuilds the descriptor
+        object.__setattr__(self, name, value)
+        object.__setattr__(self, "_desc", None)
+
+    def desc(self) -> PagePoolDesc:
+        _check_device(self.codes.device, "the pool's planes")
+        if self._desc is None:
+            object.__setattr__(self, "_desc", PagePoolDesc(
+                self.codes.data_ptr(), self.scales.data_ptr(), self.refs.data_ptr(), self.table.data_ptr(),
+                self.n_entries.data_ptr(), self.n_pages, self.page, self.n_seq, self.max_pages, self.D, self.m))
         return self._desc
 
 
@@ -336,6 +407,95 @@ def csa2_sparse_attn_decode(main: MainCache, swa: SwaCache, q, q_pos, idx, softm
                                          _ptr(idx, torch.int32), K, float(softmax_scale),
                                          _ptr(out, torch.bfloat16), _ptr(ws),
                                          0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def csa2_pages_workspace_size(pool: PagePool, n: int) -> int:
+    d = pool._desc or PagePoolDesc(None, None, None, None, None, pool.n_pages, pool.page, pool.n_seq, pool.max_pages,
+                                   pool.D, pool.m)
+    return int(lib().csa2_pages_workspace_size(ctypes.byref(d), int(n)))
+
+
+def _ws_for(ws, nbytes: int, device, stream):
+    """A caller workspace, or a fresh one that the call's own stream may keep
+    using after this function's reference to it is gone."""
+    if ws is None and nbytes:
+        ws = workspace(nbytes, device)
+        if stream is not None and ws.is_cuda:
+            ws.record_stream(torch.cuda.ExternalStream(_stream(stream), device=ws.device))
+    return ws
+
+
+def _list(t, n: int, what: str):
+    """A device list of n int32 (its length is the kernels' loop bound)."""
+    if t is not None and t.numel() != n:
+        raise ValueError(f"{what} must have {n} elements (got {t.numel()})")
+    return _ptr(t, torch.int32)
+
+
+def csa2_pages_append(pool: PagePool, src: MainCache, seq, at=None, first=None, ws=None, stream=None):
+    """Entries first[i] .. src.n_entries[i] - 1 of src's row i follow the first
+    at[i] entries of pool sequence seq[i]."""
+    ws = _ws_for(ws, csa2_pages_workspace_size(pool, src.B), pool.codes.device, stream)
+    _check(lib().csa2_pages_append(ctypes.byref(pool.desc()), ctypes.byref(src.desc()), _list(first, src.B, "first"),
+                                   _list(seq, src.B, "seq"), _list(at, src.B, "at"), _ptr(ws), _nbytes(ws),
+                                   _stream(stream)))
+
+
+def csa2_pages_fork(pool: PagePool, parent, child, ws=None, stream=None):
+    """child[i] becomes a copy of parent[i] that shares its pages (-1: emptied)."""
+    n = child.numel()
+    ws = _ws_for(ws, csa2_pages_workspace_size(pool, n), pool.codes.device, stream)
+    _check(lib().csa2_pages_fork(ctypes.byref(pool.desc()), _list(parent, n, "parent"), _list(child, n, "child"), n,
+                                 _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def csa2_pages_compact(pool: PagePool, n_live=None, ws=None, stream=None):
+    """Pages in use move below all free ones; n_live [1] gets their number."""
+    ws = _ws_for(ws, csa2_pages_workspace_size(pool, 1), pool.codes.device, stream)
+    _check(lib().csa2_pages_compact(ctypes.byref(pool.desc()), _ptr(n_live, torch.int32), _ptr(ws), _nbytes(ws),
+                                    _stream(stream)))
+
+
+def _queries(q, q_pos, out, B: int, D: int):
+    """(T_q, H) of q [B][T_q][H][D], q_pos [B][T_q], out like q."""
+    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != D or q_pos.shape != q.shape[:2] or out.shape != q.shape:
+        raise ValueError(f"q [B={B}][T_q][H][D={D}], q_pos [B][T_q] and out like q: got {tuple(q.shape)}, "
+                         f"{tuple(q_pos.shape)}, {tuple(out.shape)}")
+    return q.shape[1], q.shape[2]
+
+
+def csa2_prefix_attn_workspace_size(B: int, T_q: int, H: int, D: int) -> int:
+    return int(lib().csa2_prefix_attn_workspace_size(B, T_q, H, D))
+
+
+def csa2_prefix_attn_decode(pool: PagePool, seq, n_shared: int, swa: SwaCache | None, q, q_pos, softmax_scale: float,
+                            out, ws=None, stream=None):
+    """Attention of q [B][T_q][H][D] to every entry of the pool sequences
+    seq [B] (the first n_shared the same for all) and to the window rows."""
+    B = seq.numel()
+    T_q, H = _queries(q, q_pos, out, B, pool.D)
+    ws = _ws_for(ws, csa2_prefix_attn_workspace_size(B, T_q, H, pool.D), out.device, stream)
+    sd = ctypes.byref(swa.desc()) if swa is not None else None
+    _check(lib().csa2_prefix_attn_decode(ctypes.byref(pool.desc()), _ptr(seq, torch.int32), int(n_shared), sd,
+                                         _ptr(q, torch.bfloat16), _ptr(q_pos, torch.int32), B, T_q, H,
+                                         float(softmax_scale), _ptr(out, torch.bfloat16), _ptr(ws), _nbytes(ws),
+                                         _stream(stream)))
+
+
+def csa2_window_attn_workspace_size(B: int, T_q: int, H: int, D: int, window: int, n_sink: int = 0) -> int:
+    return int(lib().csa2_window_attn_workspace_size(B, T_q, H, D, window, n_sink))
+
+
+def csa2_window_attn(swa: SwaCache, sinks: SwaCache | None, q, q_pos, softmax_scale: float, out, ws=None, stream=None):
+    """Attention of q [B][T_q][H][D] to the window rows of swa and to the first
+    sinks.window tokens (rows of `sinks`) before them."""
+    T_q, H = _queries(q, q_pos, out, swa.B, swa.D)
+    n_sink = sinks.window if sinks is not None else 0
+    ws = _ws_for(ws, csa2_window_attn_workspace_size(swa.B, T_q, H, swa.D, swa.window, n_sink), out.device, stream)
+    kd = ctypes.byref(sinks.desc()) if sinks is not None else None
+    _check(lib().csa2_window_attn(ctypes.byref(swa.desc()), kd, _ptr(q, torch.bfloat16), _ptr(q_pos, torch.int32), T_q,
+                                  H, float(softmax_scale), _ptr(out, torch.bfloat16), _ptr(ws), _nbytes(ws),
+                                  _stream(stream)))
 
 
 def csa2_device_status(clear: bool = True, stream=None) -> int:

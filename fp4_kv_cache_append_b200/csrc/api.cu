@@ -157,6 +157,47 @@ csa2_status check_swa(const csa2_swa_cache *s) {
   return CSA2_OK;
 }
 
+csa2_status check_pool(const csa2_page_pool *p) {
+  if (!p) return fail(CSA2_ERR_INVALID_ARG, "page pool is NULL");
+  if (!p->codes || !p->scales || !p->refs || !p->table || !p->n_entries)
+    return fail(CSA2_ERR_INVALID_ARG, "page pool has a NULL plane");
+  if (!aligned16(p->codes) || !aligned16(p->scales) || !aligned16(p->refs) || !aligned16(p->table) ||
+      !aligned16(p->n_entries))
+    return fail(CSA2_ERR_INVALID_ARG, "page pool planes must be 16-byte aligned");
+  if (p->n_pages <= 0 || p->n_seq <= 0 || p->max_pages <= 0)
+    return fail(CSA2_ERR_INVALID_ARG, "page pool n_pages=%d n_seq=%d max_pages=%d", p->n_pages, p->n_seq, p->max_pages);
+  if (p->page < 16 || p->page > 4096 || p->page % 16)
+    return fail(CSA2_ERR_UNSUPPORTED_SHAPE, "page=%d must be a multiple of 16 in [16,4096]", p->page);
+  if ((int64_t)p->n_pages * p->page >= (int64_t)1 << 31 || (int64_t)p->max_pages * p->page >= (int64_t)1 << 31)
+    return fail(CSA2_ERR_UNSUPPORTED_SHAPE, "n_pages*page and max_pages*page must be < 2^31");
+  if (p->D != 128 && p->D != 256 && p->D != 512) return fail(CSA2_ERR_UNSUPPORTED_SHAPE, "page pool D=%d not in {128,256,512}", p->D);
+  if (p->m != 1 && p->m != 2) return fail(CSA2_ERR_UNSUPPORTED_SHAPE, "page pool m=%d not in {1,2}", p->m);
+  return CSA2_OK;
+}
+
+PagePoolArgs pool_args(const csa2_page_pool *p, unsigned int *status) {
+  PagePoolArgs a{};
+  a.codes = p->codes; a.scales = p->scales; a.refs = p->refs; a.table = p->table; a.n_entries = p->n_entries;
+  a.n_pages = p->n_pages; a.page = p->page; a.n_seq = p->n_seq; a.max_pages = p->max_pages; a.D = p->D; a.m = p->m;
+  a.status = status;
+  return a;
+}
+
+csa2_status check_workspace(const void *ws, size_t ws_bytes, size_t need) {
+  if (need > 0 && (!ws || ws_bytes < need || !aligned16(ws)))
+    return fail(CSA2_ERR_WORKSPACE, "workspace of %zu bytes needed (got %zu)", need, ws_bytes);
+  return CSA2_OK;
+}
+
+// The query side of the dense attentions.
+csa2_status check_queries(const uint16_t *q, const int32_t *q_pos, const uint16_t *out, int B, int T_q, int H) {
+  if (!q || !q_pos || !out || !aligned16(q) || !aligned16(q_pos) || !aligned16(out))
+    return fail(CSA2_ERR_INVALID_ARG, "q/q_pos/out must be 16-byte aligned device pointers");
+  if (B <= 0 || T_q <= 0 || (int64_t)B * T_q > 65535) return fail(CSA2_ERR_INVALID_ARG, "B=%d T_q=%d", B, T_q);
+  if (H < 1 || H > 64) return fail(CSA2_ERR_UNSUPPORTED_SHAPE, "H=%d not in [1,64]", H);
+  return CSA2_OK;
+}
+
 }  // namespace
 
 void set_last_error_message(const char *msg) { t_err = msg; }
@@ -169,7 +210,7 @@ using namespace csa2;
 
 extern "C" {
 
-int csa2_version(void) { return (1 << 16) | 0; }
+int csa2_version(void) { return (1 << 16) | 1; }
 
 const char *csa2_last_error(void) { return t_err.c_str(); }
 
@@ -588,6 +629,152 @@ csa2_status csa2_sparse_attn_decode(const csa2_main_cache *main, const csa2_swa_
   a.status = d->status;
   cudaError_t e = launch_attn(a, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? CSA2_OK : cuda_fail(e, "attention launch");
+}
+
+size_t csa2_pages_workspace_size(const csa2_page_pool *pool, int n) {
+  if (!pool || n <= 0 || n > kPageListMax || pool->n_pages <= 0 || pool->max_pages <= 0) return 0;
+  return pages_workspace_bytes(n, pool->max_pages, pool->n_pages);
+}
+
+csa2_status csa2_pages_append(const csa2_page_pool *pool, const csa2_main_cache *src, const int32_t *first,
+                              const int32_t *seq, const int32_t *at, void *ws, size_t ws_bytes, csa2_stream_t stream) {
+  t_err.clear();
+  NvtxRange nvtx("csa2_pages_append");
+  csa2_status st;
+  if ((st = check_pool(pool)) != CSA2_OK) return st;
+  if ((st = check_main(src, false)) != CSA2_OK) return st;
+  if (src->D != pool->D) return fail(CSA2_ERR_INVALID_ARG, "source D=%d, pool D=%d", src->D, pool->D);
+  if (src->codes == pool->codes || src->scales == pool->scales)
+    return fail(CSA2_ERR_INVALID_ARG, "the source and the pool share a plane");
+  if (!seq || !aligned16(seq) || (first && !aligned16(first)) || (at && !aligned16(at)))
+    return fail(CSA2_ERR_INVALID_ARG, "seq/first/at must be 16-byte aligned device pointers");
+  if (src->B > kPageListMax) return fail(CSA2_ERR_UNSUPPORTED_SHAPE, "B=%d above %d", src->B, kPageListMax);
+  if ((st = check_workspace(ws, ws_bytes, pages_workspace_bytes(src->B, pool->max_pages, pool->n_pages))) != CSA2_OK)
+    return st;
+  DeviceState *d;
+  if ((st = device_state(&d)) != CSA2_OK) return st;
+  PageAppendArgs a{};
+  a.pool = pool_args(pool, d->status);
+  a.src_codes = src->codes; a.src_scales = src->scales; a.src_n = src->n_entries;
+  a.first = first; a.seq = seq; a.at = at; a.n = src->B; a.src_cap = src->cap;
+  cudaError_t e = launch_page_append(a, ws, d->sms, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CSA2_OK : cuda_fail(e, "pages_append launch");
+}
+
+csa2_status csa2_pages_fork(const csa2_page_pool *pool, const int32_t *parent, const int32_t *child, int n, void *ws,
+                            size_t ws_bytes, csa2_stream_t stream) {
+  t_err.clear();
+  NvtxRange nvtx("csa2_pages_fork");
+  csa2_status st;
+  if ((st = check_pool(pool)) != CSA2_OK) return st;
+  if (!parent || !child || !aligned16(parent) || !aligned16(child))
+    return fail(CSA2_ERR_INVALID_ARG, "parent/child must be 16-byte aligned device pointers");
+  if (n < 1 || n > kPageListMax) return fail(CSA2_ERR_UNSUPPORTED_SHAPE, "n=%d not in [1,%d]", n, kPageListMax);
+  if ((st = check_workspace(ws, ws_bytes, pages_workspace_bytes(n, pool->max_pages, pool->n_pages))) != CSA2_OK)
+    return st;
+  DeviceState *d;
+  if ((st = device_state(&d)) != CSA2_OK) return st;
+  PageForkArgs a{pool_args(pool, d->status), parent, child, n};
+  cudaError_t e = launch_page_fork(a, ws, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CSA2_OK : cuda_fail(e, "pages_fork launch");
+}
+
+csa2_status csa2_pages_compact(const csa2_page_pool *pool, int32_t *n_live, void *ws, size_t ws_bytes,
+                               csa2_stream_t stream) {
+  t_err.clear();
+  NvtxRange nvtx("csa2_pages_compact");
+  csa2_status st;
+  if ((st = check_pool(pool)) != CSA2_OK) return st;
+  if (n_live && !aligned16(n_live)) return fail(CSA2_ERR_INVALID_ARG, "n_live must be 16-byte aligned");
+  if ((st = check_workspace(ws, ws_bytes, pages_workspace_bytes(1, pool->max_pages, pool->n_pages))) != CSA2_OK)
+    return st;
+  DeviceState *d;
+  if ((st = device_state(&d)) != CSA2_OK) return st;
+  cudaError_t e = launch_page_compact(pool_args(pool, d->status), n_live, ws, d->sms, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CSA2_OK : cuda_fail(e, "pages_compact launch");
+}
+
+static int sms_or_default() {
+  DeviceState *d;
+  return device_state(&d) == CSA2_OK ? d->sms : 148;
+}
+
+size_t csa2_prefix_attn_workspace_size(int B, int T_q, int H, int D) {
+  if (B <= 0 || T_q <= 0 || (int64_t)B * T_q > 65535 || H < 1 || H > 64 || (D != 128 && D != 256 && D != 512)) return 0;
+  return prefix_attn_workspace_bytes(B, T_q, H, D, sms_or_default());
+}
+
+csa2_status csa2_prefix_attn_decode(const csa2_page_pool *pool, const int32_t *seq, int n_shared,
+                                    const csa2_swa_cache *swa, const uint16_t *q, const int32_t *q_pos, int B, int T_q,
+                                    int H, float softmax_scale, uint16_t *out, void *ws, size_t ws_bytes,
+                                    csa2_stream_t stream) {
+  t_err.clear();
+  NvtxRange nvtx("csa2_prefix_attn_decode");
+  csa2_status st;
+  if ((st = check_pool(pool)) != CSA2_OK) return st;
+  if ((st = check_queries(q, q_pos, out, B, T_q, H)) != CSA2_OK) return st;
+  if (!seq || !aligned16(seq)) return fail(CSA2_ERR_INVALID_ARG, "seq must be a 16-byte aligned device pointer");
+  if (n_shared < 0 || n_shared > (int64_t)pool->max_pages * pool->page)
+    return fail(CSA2_ERR_INVALID_ARG, "n_shared=%d outside the table's %d pages", n_shared, pool->max_pages);
+  if (swa) {
+    if ((st = check_swa(swa)) != CSA2_OK) return st;
+    if (swa->B != B || swa->D != pool->D) return fail(CSA2_ERR_INVALID_ARG, "window cache and pool or batch disagree");
+  }
+  DeviceState *d;
+  if ((st = device_state(&d)) != CSA2_OK) return st;
+  if ((st = check_workspace(ws, ws_bytes, prefix_attn_workspace_bytes(B, T_q, H, pool->D, d->sms))) != CSA2_OK) return st;
+  DenseAttnArgs a{};
+  a.pool = pool_args(pool, d->status);
+  a.seq = seq; a.n_shared = n_shared;
+  if (swa && swa->window > 0) {
+    a.swa_rows = swa->rows; a.s_swa = swa->scale; a.W_cap = swa->W_cap; a.window = swa->window;
+  }
+  a.q = q; a.q_pos = q_pos; a.B = B; a.T_q = T_q; a.H = H; a.D = pool->D;
+  a.scale = softmax_scale; a.out = out; a.ws = ws; a.status = d->status;
+  cudaError_t e = launch_prefix_attn(a, d->sms, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CSA2_OK : cuda_fail(e, "prefix attention launch");
+}
+
+size_t csa2_window_attn_workspace_size(int B, int T_q, int H, int D, int window, int n_sink) {
+  if (B <= 0 || T_q <= 0 || (int64_t)B * T_q > 65535 || H < 1 || H > 64 || (D != 128 && D != 256 && D != 512) ||
+      window < 0 || window > 1024 || n_sink < 0 || n_sink > 1024)
+    return 0;
+  return window_attn_workspace_bytes(B, T_q, H, D, window, n_sink, sms_or_default());
+}
+
+csa2_status csa2_window_attn(const csa2_swa_cache *swa, const csa2_swa_cache *sinks, const uint16_t *q,
+                             const int32_t *q_pos, int T_q, int H, float softmax_scale, uint16_t *out, void *ws,
+                             size_t ws_bytes, csa2_stream_t stream) {
+  t_err.clear();
+  NvtxRange nvtx("csa2_window_attn");
+  csa2_status st;
+  if (!swa) return fail(CSA2_ERR_INVALID_ARG, "window cache is NULL");
+  if ((st = check_swa(swa)) != CSA2_OK) return st;
+  if (sinks) {
+    if ((st = check_swa(sinks)) != CSA2_OK) return st;
+    if (sinks->B != swa->B || sinks->D != swa->D) return fail(CSA2_ERR_INVALID_ARG, "sinks and window cache disagree");
+  }
+  if ((st = check_queries(q, q_pos, out, swa->B, T_q, H)) != CSA2_OK) return st;
+  if (swa->window > 0 && swa->W_cap < (int64_t)T_q + swa->window - 1)
+    return fail(CSA2_ERR_INVALID_ARG, "W_cap=%d: a chunk of %d tokens needs %lld rows", swa->W_cap, T_q,
+                (long long)T_q + swa->window - 1);
+  const int n_sink = sinks ? sinks->window : 0;
+  DeviceState *d;
+  if ((st = device_state(&d)) != CSA2_OK) return st;
+  if ((st = check_workspace(ws, ws_bytes, window_attn_workspace_bytes(swa->B, T_q, H, swa->D, swa->window, n_sink,
+                                                                      d->sms))) != CSA2_OK)
+    return st;
+  DenseAttnArgs a{};
+  if (swa->window > 0) {
+    a.swa_rows = swa->rows; a.s_swa = swa->scale; a.W_cap = swa->W_cap; a.window = swa->window;
+  }
+  if (n_sink > 0) {
+    a.sink_rows = sinks->rows; a.s_sink = sinks->scale; a.n_sink = n_sink; a.sink_cap = sinks->W_cap;
+  }
+  a.q = q; a.q_pos = q_pos; a.B = swa->B; a.T_q = T_q; a.H = H; a.D = swa->D;
+  a.scale = softmax_scale; a.out = out; a.ws = ws; a.status = d->status;
+  cudaError_t e = launch_window_attn(a, d->sms, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CSA2_OK : cuda_fail(e, "window attention launch");
 }
 
 }  // extern "C"

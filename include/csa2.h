@@ -29,9 +29,9 @@
  *  - bf16 tensors are passed as their 16-bit patterns (uint16_t).
  *  - Device pointers must be 16-byte aligned.
  *  - In-kernel anomalies (an index outside the cache, a ring position below
- *    zero, a bounded wait that ran out) never trap: the offending item is
- *    masked and a bit is set in the library's device status word, read with
- *    csa2_device_status().
+ *    zero, a bounded wait that ran out, too few free pages) never trap: the
+ *    offending item is masked and a bit is set in the library's device status
+ *    word, read with csa2_device_status().
  *  - Inputs with NaN or Inf are not supported (results unspecified, no trap).
  *  - The library looks up, once per device, the device addresses of its own
  *    global arrays (the status word; entry 6's scratch).  A process that
@@ -72,6 +72,8 @@ typedef enum {
 #define CSA2_DEV_TIMEOUT       0x2u  /* a bounded pipeline wait gave up (tile skipped)              */
 #define CSA2_DEV_APPEND_RANGE  0x4u  /* an appended entry fell beyond cap (not written)             */
 #define CSA2_DEV_BAD_POSITION  0x8u  /* a negative token position (item skipped)                    */
+#define CSA2_DEV_NO_PAGE       0x10u /* a paged append found too few free pages or table slots (its sequence left as it was) */
+#define CSA2_DEV_BAD_SEQUENCE  0x20u /* a listed sequence out of range, twice the target, or cut behind its end (skipped)    */
 
 /*
  * Main (global) FP4 KV cache of one CSA2 layer group [jaehun "3) FP4 ...":
@@ -368,6 +370,124 @@ CSA2_API csa2_status csa2_topk_noalloc(const float *scores, int rows, int64_t ld
                                        const int32_t *n_valid, const int32_t *pool_blocks, int K,
                                        int32_t *out_idx, int P_out, int32_t *out_pool,
                                        csa2_stream_t stream);
+
+/*
+ * Paged FP4 cache: entries of many sequences in pages that sequences can
+ * share.  (No counterpart in the paper: the serving side of its FP4 main KV,
+ * for layers that attend to all their entries -- before a context is longer
+ * than the Top-K, or without an indexer.)  Everything is device memory, so
+ * appending, forking and freeing never wait for the host and can be captured
+ * into graphs.
+ *   codes     [n_pages][page][D/2]  u8 E2M1 pairs, as in csa2_main_cache
+ *   scales    [n_pages][page][D/16] u8 E4M3
+ *   refs      [n_pages] i32: table slots that hold the page; 0 = free
+ *   table     [n_seq][max_pages] i32: page of a sequence's i-th `page`
+ *             entries, -1 = none (every slot behind the last used one)
+ *   n_entries [n_seq] i32
+ * An empty pool is refs = 0, table = -1, n_entries = 0.
+ * m: tokens per entry, 1 or 2 (only the attention's visibility uses it).
+ * Supported: D in {128, 256, 512}; page a multiple of 16 in [16, 4096];
+ * n_pages * page < 2^31.
+ */
+typedef struct {
+    uint8_t *codes;
+    uint8_t *scales;
+    int32_t *refs;
+    int32_t *table;
+    int32_t *n_entries;
+    int32_t n_pages, page, n_seq, max_pages, D, m;
+} csa2_page_pool;
+
+/*
+ * 7. Paged append: entries of a contiguous cache go into pages.
+ *  src    main cache [B][cap] whose codes, scales and n_entries are read (D as
+ *         the pool's): row i gives entries first[i] .. n_entries[i] - 1
+ *  first  [B] i32 DEVICE (NULL = 0 for all)
+ *  seq    [B] i32 DEVICE: pool sequence each row goes to, -1 = none
+ *  at     [B] i32 DEVICE: the sequence is cut to `at` entries and the new ones
+ *         follow, so a repeated call gives the same cache and rejected tokens
+ *         are cut off by the next append (NULL = its n_entries)
+ *  ws, ws_bytes: csa2_pages_workspace_size(pool, B) bytes
+ * A page is never written while another table slot holds it: a shared partial
+ * last page is replaced by a fresh one with its first at % page entries
+ * copied.  Fresh pages are the lowest-numbered ones that are free when the
+ * call starts, in the order of the list; pages no longer needed are released
+ * (free from the next call on).  A sequence that finds too few pages or table
+ * slots stays as it was (CSA2_DEV_NO_PAGE); the pages it would have taken
+ * stay reserved within the call.  A sequence listed twice is appended to
+ * once, for its first listing (CSA2_DEV_BAD_SEQUENCE).
+ * Supported: B <= 4096.
+ */
+CSA2_API csa2_status csa2_pages_append(const csa2_page_pool *pool, const csa2_main_cache *src, const int32_t *first,
+                                       const int32_t *seq, const int32_t *at, void *ws, size_t ws_bytes,
+                                       csa2_stream_t stream);
+CSA2_API size_t csa2_pages_workspace_size(const csa2_page_pool *pool, int n);
+
+/*
+ * 8. Fork and free: sequence child[i] becomes a copy of parent[i] that shares
+ *    its pages (no entry moves); what child[i] held is released.  parent[i] =
+ *    -1 empties child[i].  All parents are taken as they stand when the call
+ *    starts, so one call can permute or replace sequences (a beam step).  A
+ *    child listed twice is set once, by its first listing
+ *    (CSA2_DEV_BAD_SEQUENCE).
+ *  parent, child [n] i32 DEVICE; ws: csa2_pages_workspace_size(pool, n) bytes
+ * Supported: 1 <= n <= 4096.
+ */
+CSA2_API csa2_status csa2_pages_fork(const csa2_page_pool *pool, const int32_t *parent, const int32_t *child, int n,
+                                     void *ws, size_t ws_bytes, csa2_stream_t stream);
+
+/*
+ * 9. Compact: with L pages in use, those at L and above move into the free
+ *    ones below L (the k-th of the one to the k-th of the other) and every
+ *    table follows, so that pages L .. n_pages - 1 are free.
+ *  n_live i32 DEVICE out (may be NULL): L
+ *  ws: csa2_pages_workspace_size(pool, 1) bytes
+ */
+CSA2_API csa2_status csa2_pages_compact(const csa2_page_pool *pool, int32_t *n_live, void *ws, size_t ws_bytes,
+                                        csa2_stream_t stream);
+
+/*
+ * 10. Attention to every entry of paged sequences, a shared prefix computed
+ *     once for the whole batch.
+ *  pool   the entries; seq [B] i32 DEVICE: pool sequence of each batch row
+ *  n_shared (host) entries that the batch's sequences have in common: they are
+ *         read once, through the table of seq[0] (0 = nothing is shared).
+ *         That the sequences agree on them is the caller's word; a sequence
+ *         with fewer entries sees only its own number of them.
+ *  swa    window cache of the layer with B rows (NULL: no window)
+ *  q      [B][T_q][H][D] bf16, q_pos [B][T_q] i32 token position t of each query
+ *  out    [B][T_q][H][D] bf16: softmax over the entries e < min(n_entries,
+ *         floor((t+1)/m)) of the sequence and the window rows of tokens
+ *         max(0,t-window+1)..t, of scale * q . x^, FP32 accumulation; zeros
+ *         when that set is empty (a padded query: t = -1)
+ *  ws, ws_bytes: csa2_prefix_attn_workspace_size(B, T_q, H, D) bytes
+ * |q| must be below 65,504 (the products run in fp16).
+ * Supported: 1 <= H <= 64, B * T_q <= 65,535, window <= 1024.
+ */
+CSA2_API csa2_status csa2_prefix_attn_decode(const csa2_page_pool *pool, const int32_t *seq, int n_shared,
+                                             const csa2_swa_cache *swa, const uint16_t *q, const int32_t *q_pos, int B,
+                                             int T_q, int H, float softmax_scale, uint16_t *out, void *ws,
+                                             size_t ws_bytes, csa2_stream_t stream);
+CSA2_API size_t csa2_prefix_attn_workspace_size(int B, int T_q, int H, int D);
+
+/*
+ * 11. Sliding-window attention whose first tokens stay visible (sinks), for
+ *     the window-only layers [jaehun "새로운 접근법": layers 1-2 use
+ *     sliding-window attention only]: prefill chunks and single tokens.
+ *  swa    the layer's window ring (a chunk of T_q tokens needs
+ *         W_cap >= T_q + window - 1, as for the append)
+ *  sinks  (may be NULL) the first tokens' rows: token s in row s, for
+ *         s < sinks->window (filled by csa2_append_quant into this cache when
+ *         the sequence's first tokens arrive); its own scale
+ *  q, q_pos, out as for entry 10; a query at t sees the tokens
+ *         max(0,t-window+1)..t and the sinks before them (no token twice)
+ *  ws, ws_bytes: csa2_window_attn_workspace_size(...) bytes
+ * |q| must be below 65,504.  Supported: as for entry 10.
+ */
+CSA2_API csa2_status csa2_window_attn(const csa2_swa_cache *swa, const csa2_swa_cache *sinks, const uint16_t *q,
+                                      const int32_t *q_pos, int T_q, int H, float softmax_scale, uint16_t *out,
+                                      void *ws, size_t ws_bytes, csa2_stream_t stream);
+CSA2_API size_t csa2_window_attn_workspace_size(int B, int T_q, int H, int D, int window, int n_sink);
 
 /* Diagnostic: with polls > 0, the MMA-issuing warp of every later indexer
  * scan (csa2_index_full, _prepared, _topk, _reindex) first waits `polls`
