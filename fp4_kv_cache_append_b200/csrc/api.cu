@@ -168,8 +168,8 @@ csa2_status check_pool(const csa2_page_pool *p) {
     return fail(CSA2_ERR_INVALID_ARG, "page pool n_pages=%d n_seq=%d max_pages=%d", p->n_pages, p->n_seq, p->max_pages);
   if (p->page < 16 || p->page > 4096 || p->page % 16)
     return fail(CSA2_ERR_UNSUPPORTED_SHAPE, "page=%d must be a multiple of 16 in [16,4096]", p->page);
-  if ((int64_t)p->n_pages * p->page >= (int64_t)1 << 31 || (int64_t)p->max_pages * p->page >= (int64_t)1 << 31)
-    return fail(CSA2_ERR_UNSUPPORTED_SHAPE, "n_pages*page and max_pages*page must be < 2^31");
+  if ((int64_t)p->n_pages * p->page >= (int64_t)1 << 31 || (int64_t)p->max_pages * p->page > (int64_t)1 << 30)
+    return fail(CSA2_ERR_UNSUPPORTED_SHAPE, "n_pages*page must be < 2^31, max_pages*page <= 2^30");
   if (p->D != 128 && p->D != 256 && p->D != 512) return fail(CSA2_ERR_UNSUPPORTED_SHAPE, "page pool D=%d not in {128,256,512}", p->D);
   if (p->m != 1 && p->m != 2) return fail(CSA2_ERR_UNSUPPORTED_SHAPE, "page pool m=%d not in {1,2}", p->m);
   return CSA2_OK;
@@ -189,11 +189,13 @@ csa2_status check_workspace(const void *ws, size_t ws_bytes, size_t need) {
   return CSA2_OK;
 }
 
-// The query side of the dense attentions.
-csa2_status check_queries(const uint16_t *q, const int32_t *q_pos, const uint16_t *out, int B, int T_q, int H) {
+// The query side of the dense attentions (rows = queries x heads stay far inside 32 bits).
+constexpr int64_t kWindowMaxQueries = 1 << 22;
+csa2_status check_queries(const uint16_t *q, const int32_t *q_pos, const uint16_t *out, int B, int T_q, int H,
+                          int64_t most_queries) {
   if (!q || !q_pos || !out || !aligned16(q) || !aligned16(q_pos) || !aligned16(out))
     return fail(CSA2_ERR_INVALID_ARG, "q/q_pos/out must be 16-byte aligned device pointers");
-  if (B <= 0 || T_q <= 0 || (int64_t)B * T_q > 65535) return fail(CSA2_ERR_INVALID_ARG, "B=%d T_q=%d", B, T_q);
+  if (B <= 0 || T_q <= 0 || (int64_t)B * T_q > most_queries) return fail(CSA2_ERR_INVALID_ARG, "B=%d T_q=%d", B, T_q);
   if (H < 1 || H > 64) return fail(CSA2_ERR_UNSUPPORTED_SHAPE, "H=%d not in [1,64]", H);
   return CSA2_OK;
 }
@@ -712,7 +714,7 @@ csa2_status csa2_prefix_attn_decode(const csa2_page_pool *pool, const int32_t *s
   NvtxRange nvtx("csa2_prefix_attn_decode");
   csa2_status st;
   if ((st = check_pool(pool)) != CSA2_OK) return st;
-  if ((st = check_queries(q, q_pos, out, B, T_q, H)) != CSA2_OK) return st;
+  if ((st = check_queries(q, q_pos, out, B, T_q, H, 65535)) != CSA2_OK) return st;
   if (!seq || !aligned16(seq)) return fail(CSA2_ERR_INVALID_ARG, "seq must be a 16-byte aligned device pointer");
   if (n_shared < 0 || n_shared > (int64_t)pool->max_pages * pool->page)
     return fail(CSA2_ERR_INVALID_ARG, "n_shared=%d outside the table's %d pages", n_shared, pool->max_pages);
@@ -736,8 +738,8 @@ csa2_status csa2_prefix_attn_decode(const csa2_page_pool *pool, const int32_t *s
 }
 
 size_t csa2_window_attn_workspace_size(int B, int T_q, int H, int D, int window, int n_sink) {
-  if (B <= 0 || T_q <= 0 || (int64_t)B * T_q > 65535 || H < 1 || H > 64 || (D != 128 && D != 256 && D != 512) ||
-      window < 0 || window > 1024 || n_sink < 0 || n_sink > 1024)
+  if (B <= 0 || T_q <= 0 || (int64_t)B * T_q > kWindowMaxQueries || H < 1 || H > 64 ||
+      (D != 128 && D != 256 && D != 512) || window < 0 || window > 1024 || n_sink < 0 || n_sink > 1024)
     return 0;
   return window_attn_workspace_bytes(B, T_q, H, D, window, n_sink, sms_or_default());
 }
@@ -754,7 +756,7 @@ csa2_status csa2_window_attn(const csa2_swa_cache *swa, const csa2_swa_cache *si
     if ((st = check_swa(sinks)) != CSA2_OK) return st;
     if (sinks->B != swa->B || sinks->D != swa->D) return fail(CSA2_ERR_INVALID_ARG, "sinks and window cache disagree");
   }
-  if ((st = check_queries(q, q_pos, out, swa->B, T_q, H)) != CSA2_OK) return st;
+  if ((st = check_queries(q, q_pos, out, swa->B, T_q, H, kWindowMaxQueries)) != CSA2_OK) return st;
   if (swa->window > 0 && swa->W_cap < (int64_t)T_q + swa->window - 1)
     return fail(CSA2_ERR_INVALID_ARG, "W_cap=%d: a chunk of %d tokens needs %lld rows", swa->W_cap, T_q,
                 (long long)T_q + swa->window - 1);

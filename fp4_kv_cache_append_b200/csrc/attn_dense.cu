@@ -1,11 +1,51 @@
-// Dense attentions: all entries of paged FP4 sequences, and the sliding
-// window with its first tokens.  One softmax per (query, head) over every
-// visible key, K = V shared by the heads.
+// Dense attentions: all entries of paged FP4 sequences (a prefix that the
+// batch shares computed once), and the sliding window with its first tokens.
+// One softmax per (query, head) over every visible key, K = V shared by the
+// heads:  out = sum_k softmax_k(scale q . x_k) x_k.
 //
-// First form: a block per (query, 8 heads), one warp per head; the block's
-// keys are dequantised to fp32 tiles of 32 in shared memory, lane = key for
-// the logits and lane = channel for the values, with the running maximum and
-// sum of the softmax in registers.
+// Because all heads (and, over a shared prefix, all sequences) meet the same
+// keys, 128 flattened (query, head) rows form the M of the matrix products
+// whatever their number of heads: S = Q K^T (M 128, N 64 keys, K 16 x D / 16)
+// and O += P V (M 128, N up to 256 channels).  For D = 512 the O of 128 rows
+// fills the tensor memory, so two blocks take 256 channels each and both form
+// S.
+//
+// One persistent block per SM; keys in tiles of 64.  Warp roles, handing work
+// over through mbarriers:
+//   warp 13     loads (cp.async) the raw bytes of a step (256 channels of a
+//               tile's FP4 codes and scales, or 128 of its FP8 rows), whatever
+//               pages its keys lie in, into one of three stages
+//   warps 0-7   dequantise, exactly, to fp16 into a ring of chunk groups
+//               (64-channel chunks, K-major, 128B swizzle); two teams of four
+//               warps take the groups in turn.  The chunks that only S needs
+//               come first and are freed first
+//   warps 8-11  softmax, one row per thread: no exchange between threads.  The
+//               reference maximum moves only when a logit exceeds it by 2^15;
+//               O is then rescaled in tensor memory.  P goes back to tensor
+//               memory (fp16) as the A operand of the second product
+//   warps 12, 14  tcgen05.mma issuers of S and of O, one lane each: S of tile
+//               i + 1 runs during tile i's softmax, O of tile i as soon as its P
+//               is there
+//   warp 15     writes the next segment (see below) while this one runs
+// Up to four chunks of Q (256 channels) are kept in tensor memory as the A
+// operand, the rest in shared memory: shared-memory bandwidth bounds the S
+// product (128 rows of A and 64 of B per K step of 16 take 48 cycles against
+// 32 of the tensor core), and the room it leaves holds the stages and a fourth
+// ring group (with three, the fetch of a tile waits for the O product of the
+// tile two before it).  S has two buffers, since about 700 cycles pass between
+// the last MMA of a tile and the first of the next that waited for it; P
+// replaces its tile's S.
+// Rows are given by unit (128 rows x a list of keys); a unit's key list is
+// split over blocks wherever the even division of all tiles over the SMs cuts
+// it, each part leaving (O, max, sum) in the workspace for a merge kernel.
+// Window rows enter unscaled: their scale multiplies the logits, and O is
+// converted once where the key list changes from one scale to another.
+// Each role runs its own loop over the block's segments and meets the others
+// at named barriers, so that the registers can be divided between the roles.
+// Every wait is bounded: one that gives up flags the device status and stops
+// every role; issued MMAs are drained and TMEM freed before the block exits.
+#include <limits.h>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -13,142 +53,1222 @@ namespace csa2 {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kKeys = 32;
-
-// Row of the pool's planes that holds entry e of pool sequence s, or -1.
-__device__ __forceinline__ int pool_slot(const DenseAttnArgs &a, int s, int e) {
-  const int pg = a.pool.table[(size_t)s * a.pool.max_pages + e / a.pool.page];
-  if (pg < 0 || pg >= a.pool.n_pages) {
-    flag(a.status, CSA2_DEV_INDEX_RANGE);
-    return -1;
-  }
-  return pg * a.pool.page + e % a.pool.page;
-}
+constexpr int kDqWarps = 8;
+constexpr int kDq = kDqWarps * 32, kTeam = kDqWarps / 2;   // dequantise threads; warps of a team
+constexpr int kSmWarp0 = 8;                  // softmax warps 8..11
+constexpr int kMmaWarp = 12;
+constexpr int kTile = 64;                    // keys per tile
+constexpr int kThreads = 16 * 32;            // four warpgroups: registers are split between them
+constexpr int kSegBar = 1, kQBar = 2;        // named barriers: a segment's start and end (all threads); Q in place
+constexpr int kSchedWarp = 15;               // writes the next segment
+// Registers per thread of the warpgroups: 2 x fetch, softmax, MMA (a tile's
+// logits stay in registers; a spill would go to L2, shared memory takes all of
+// the L1's room).  Their sum is at most the launch's 4 x 128.
+constexpr int kRegsFetch = 88, kRegsSoftmax = 208, kRegsMma = 128;
+constexpr int kLoadWarp = 13;                // loader: lane = keys lane and lane + 32
+constexpr int kPvWarp = 14;                  // MMA issuer of O (kMmaWarp: of S)
+constexpr int kStages = 3;                   // raw steps in flight or in use
+// A stage: 64 rows of 128 bytes (codes, or FP8 values), then 64 x 16 of scales.
+constexpr int kRawRow = 128, kRawSc = kTile * kRawRow, kRawScRow = 16, kRawBytes = kRawSc + kTile * kRawScRow;
+constexpr int kRows = 128;                   // rows per unit
+constexpr int kUnitCost = 5;                 // see Schedule::ov: 12k cycles at 2.7k a tile (D 512)
+constexpr int kMaxQ = kRows + 1;             // queries that 128 rows can touch
+constexpr int kMaxPos = INT_MAX - 4096;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLazy = 15.0f;               // log2 headroom of P below fp16's 65,504
+constexpr uint32_t kWaitLimit = 1u << 22;
+// TMEM columns: O, S of two tiles (each later its P), Q's first chunks
+constexpr uint32_t kColO = 0, kColS = 256, kColQ = 384, kTmemCols = 512;
 
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) attn_dense_simple_kernel(const DenseAttnArgs a) {
-  extern __shared__ float sm[];
-  float *kt = sm;                       // [32][D + 1]
-  float *qs = sm + kKeys * (D + 1);     // [8][D]
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int row = blockIdx.x, b = row / a.T_q, h = blockIdx.y * kWarps + warp;
-  pdl_launch_dependents();
-  pdl_wait();
-  const int t = a.q_pos[row];
-  for (int c = lane; c < D; c += 32)
-    qs[warp * D + c] = h < a.H ? bf16_to_f32(a.q[((size_t)row * a.H + h) * D + c]) * a.scale : 0.f;
-  float o[D / 32];
-#pragma unroll
-  for (int u = 0; u < D / 32; ++u) o[u] = 0.f;
-  float m = -INFINITY, l = 0.f;
+struct Cfg {
+  static constexpr int DO = D < 256 ? D : 256;           // output channels of a block
+  static constexpr int CS = D / DO;                      // blocks that share a unit's channels
+  static constexpr int NCH = D / 64;                     // 64-channel chunks of a key
+  static constexpr int GC = DO / 64;                     // chunks of a ring group
+  static constexpr int NG = D == 128 ? 8 : 4;             // ring groups
+  static constexpr int QT = NCH < 4 ? NCH : 4;           // chunks of Q in tensor memory, the first in S's order
+  static constexpr int QS = NCH - QT;                    // ... in shared memory
+};
 
-  int n_ent = 0, s = -1;
-  if (a.pool.codes && t >= 0) {
-    s = a.seq[b];
-    if (s < 0 || s >= a.pool.n_seq) {
-      flag(a.status, CSA2_DEV_BAD_SEQUENCE);
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+
+// What a block does next: a part of a unit's key list.
+struct Segment {
+  int half;                // channel half
+  int b;                   // batch row of the keys (0 over the shared prefix)
+  int row0;                // first flattened row
+  int nrows;
+  int n_sink, n_fp4, n_win;   // tiles of each sort, in this order
+  int key0;                // first entry of the first FP4 tile
+  int key_end;             // entries from here on are not read
+  int seq;                 // pool sequence whose table is read (-1: none)
+  int slot;                // partial result's place, -1: straight to the output
+  int q0, nq;              // queries of the rows
+  int pos[kMaxQ];          // their token positions
+};
+
+template <int D>
+struct DenseSmem {
+  alignas(1024) uint8_t q[(Cfg<D>::QS > 0 ? Cfg<D>::QS : 1) * kRows * 128];       // chunks of [128 rows x 128 B]
+  alignas(1024) uint8_t kv[Cfg<D>::NG][Cfg<D>::GC * kTile * 128];                // groups of chunks [64 keys x 128 B]
+  alignas(16) uint8_t raw[kStages][kRawBytes];
+  uint64_t raw_full[kStages], raw_empty[kStages];
+  uint64_t full[Cfg<D>::NG];
+  uint64_t empty[Cfg<D>::NG];
+  uint64_t s_full[2], p_full[2], pv_done[2], fin;                                // of a tile's buffer
+  uint32_t tmem_base;
+  int abort;
+  int more[2];
+  Segment seg[2];                                                                // this one and the next
+};
+
+__device__ __forceinline__ uint32_t sw_off(int r, int pc, int rows) {   // 16-byte piece pc of row r
+  return (uint32_t)((pc >> 3) * rows * 128 + r * 128 + (((pc & 7) ^ (r & 7)) << 4));
+}
+
+// Place of 16-byte piece pc of row r in a raw stage: eight lanes that read 4
+// rows x 2 neighbouring pieces meet eight different columns.
+__device__ __forceinline__ uint32_t raw_off(int r, int pc) {
+  return (uint32_t)(r * kRawRow + ((pc ^ ((r & 3) << 1)) << 4));
+}
+
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Asynchronous copies to shared memory; `live` false writes zeros instead.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void *src, bool live) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(live ? BYTES : 0), "n"(BYTES)
+                 : "memory");
+}
+// Arrive on `bar` once this thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void mbar_arrive_n(uint64_t *bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
+
+// Two fp32 operations per instruction.
+__device__ __forceinline__ uint64_t f32x2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f32x2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort) {
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 255u) == 255u && *abort) return false;
+  }
+  *abort = 1;
+  return false;
+}
+
+// The next stretch of at most 64 window tokens at or behind `cur` that the
+// unit's queries see, every token of it seen by one of them (what lies between
+// their windows is never read).  Called by converged warps; false: none.
+__device__ __forceinline__ bool next_window(const Segment &sg, int window, int cur, int lane, int *start, int *end) {
+  int lo = INT_MAX;
+#pragma unroll 1
+  for (int i = lane; i < sg.nq; i += 32) {
+    const int t = sg.pos[i];
+    if (t >= 0 && t >= cur) {
+      int l = t - window + 1;
+      l = l < cur ? cur : l;
+      l = l < 0 ? 0 : l;
+      lo = l < lo ? l : lo;
+    }
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  if (lo == INT_MAX) return false;
+  int e = lo;
+#pragma unroll 1
+  while (e < lo + kTile) {
+    int m = e;
+#pragma unroll 1
+    for (int i = lane; i < sg.nq; i += 32) {
+      const int t = sg.pos[i];
+      if (t >= e && t - window + 1 <= e) m = t + 1 > m ? t + 1 : m;
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (m == e) break;
+    e = m;
+  }
+  *start = lo;
+  *end = e < lo + kTile ? e : lo + kTile;
+  return true;
+}
+
+// Division of non-negative numbers that nearly always fit 32 bits.
+__device__ __forceinline__ long long div64(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// ------------------------------------------------------------------ schedule of the prefix attention
+
+struct Schedule {
+  int rt_sh, nt_sh;        // row tiles over all rows; key tiles of the prefix
+  int rt_own;              // row tiles of a sequence
+  int wt;                  // tiles that a window counts for
+  int ov;                  // tiles' worth of time that starting and ending a unit takes
+  int units;               // units of a channel half
+  int cs;
+  int grid;
+};
+
+__host__ __device__ __forceinline__ Schedule make_schedule(const DenseAttnArgs &a, int cs, int grid) {
+  Schedule s;
+  const long long rows = (long long)a.B * a.T_q * a.H;
+  s.rt_sh = (int)((rows + kRows - 1) / kRows);
+  s.nt_sh = (a.n_shared + kTile - 1) / kTile;
+  s.rt_own = (a.T_q * a.H + kRows - 1) / kRows;
+  s.wt = a.window > 0 ? (a.window + kTile - 1) / kTile : 0;
+  s.ov = kUnitCost;
+  s.units = s.rt_sh + a.B * s.rt_own;
+  s.cs = cs;
+  s.grid = grid;
+  return s;
+}
+
+// The linear order of all tiles of a channel half: the prefix's row tiles, then
+// the sequences' own row tiles; a unit's length is ov + FP4 tiles + wt.
+__host__ __device__ __forceinline__ long long shared_length(const Schedule &s) {
+  return s.nt_sh > 0 ? (long long)s.ov + s.nt_sh : 0;
+}
+__device__ __forceinline__ long long own_length(const Schedule &s, int own) {
+  return own + s.wt > 0 ? (long long)s.ov + own + s.wt : 0;
+}
+
+// Pool sequence of batch row b (-1 when out of range) and its entries.
+__device__ __forceinline__ int seq_entries(const DenseAttnArgs &a, int b, int *n) {
+  const int s = a.seq[b];
+  *n = 0;
+  if (s < 0 || s >= a.pool.n_seq) return -1;
+  const long long room = (long long)a.pool.max_pages * a.pool.page;
+  const int v = a.pool.n_entries[s];
+  *n = v < 0 ? 0 : (v > room ? (int)room : v);
+  return s;
+}
+__device__ __forceinline__ int own_tiles(const DenseAttnArgs &a, int b) {
+  int n;
+  seq_entries(a, b, &n);
+  return n > a.n_shared ? (n - a.n_shared + kTile - 1) / kTile : 0;
+}
+
+// Workspace: per unit {first slot, slots}, per slot [128] (max, sum), per slot
+// [DO / 4][128] float4 of O.
+struct DenseWs {
+  size_t off_ml, off_o, bytes;
+};
+__host__ __device__ __forceinline__ DenseWs dense_ws(long long units, int grid, int DO) {
+  DenseWs w;
+  const long long slots = units + grid;
+  w.off_ml = ((size_t)units * 8 + 255) & ~size_t(255);
+  w.off_o = w.off_ml + (size_t)slots * kRows * 8;
+  w.bytes = w.off_o + (size_t)slots * kRows * DO * 4;
+  return w;
+}
+
+// Warp 0: the segment at linear position *x (before x_end); advances *x.
+__device__ __forceinline__ bool next_prefix_segment(const DenseAttnArgs &a, const Schedule &sc, long long th, long long chunk,
+                                    long long *x, long long x_end, int lane, Segment &sg) {
+#pragma unroll 1
+  while (*x < x_end) {
+    const int half = *x >= th ? 1 : 0;   // at most two channel halves
+    const long long base = (long long)half * th;
+    long long y = *x - base;
+    const long long one = shared_length(sc), sh = sc.rt_sh * one;
+    int unit, nt, wt, b = 0, rt;
+    long long tile, unit_at;
+    if (y < sh) {
+      rt = (int)div64(y, one);
+      unit = rt; tile = y - rt * one - sc.ov; nt = sc.nt_sh; wt = 0;
+      unit_at = base + rt * one;
     } else {
-      n_ent = a.pool.n_entries[s];
-      const int vis = (t + 1) / a.pool.m, room = a.pool.max_pages * a.pool.page;
-      n_ent = n_ent < vis ? n_ent : vis;
-      n_ent = n_ent < room ? n_ent : room;
-    }
-  }
-  const int s0 = a.pool.codes ? a.seq[0] : -1;
-  int wlo = t - a.window + 1;
-  if (wlo < 0) wlo = 0;
-  const int n_win = a.swa_rows && a.window > 0 && t >= 0 ? t - wlo + 1 : 0;
-  const int n_snk = a.sink_rows && t >= 0 ? (a.n_sink < wlo ? a.n_sink : wlo) : 0;
-  const int total = n_ent + n_snk + n_win;
-
-  for (int k0 = 0; k0 < total; k0 += kKeys) {
-    __syncthreads();
-    for (int i = tid; i < kKeys * (D / 16); i += kWarps * 32) {   // 16 channels of a key per item
-      const int r = i / (D / 16), g = i % (D / 16), k = k0 + r;
-      float v[16];
-      bool have = false;
-      if (k < n_ent) {
-        const int sq = k < a.n_shared && s0 >= 0 && s0 < a.pool.n_seq ? s0 : s;
-        const int at = pool_slot(a, sq, k);
-        if (at >= 0) {
-          have = true;
-          const float sc = e4m3_to_f32(a.pool.scales[(size_t)at * (D / 16) + g]);
-          const uint2 w = *reinterpret_cast<const uint2 *>(a.pool.codes + (size_t)at * (D / 2) + 8 * g);
+      y -= sh;
+      long long at = 0;     // linear position of sequence b0 within the own part
+      int b0 = 0, own = 0;
+#pragma unroll 1
+      for (;;) {
+        const int bb = b0 + lane;
+        own = bb < a.B ? own_tiles(a, bb) : 0;
+        const long long c = bb < a.B ? sc.rt_own * own_length(sc, own) : 0;
+        long long inc = c;
 #pragma unroll
-          for (int u = 0; u < 16; ++u) v[u] = e2m1_to_f32(((u < 8 ? w.x : w.y) >> (4 * (u & 7))) & 15u) * sc;
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += v;
         }
-      } else if (k < total) {
-        have = true;
-        const bool snk = k < n_ent + n_snk;
-        const uint8_t *p = snk ? a.sink_rows + ((size_t)b * a.sink_cap + (k - n_ent)) * D
-                               : a.swa_rows + ((size_t)b * a.W_cap + (wlo + k - n_ent - n_snk) % a.W_cap) * D;
-        const float sc = snk ? a.s_sink : a.s_swa;
-#pragma unroll
-        for (int u = 0; u < 16; ++u) v[u] = e4m3_to_f32(p[16 * g + u]) * sc;
+        const uint32_t hit = __ballot_sync(0xffffffffu, at + inc > y);
+        if (hit) {
+          const int l = __ffs(hit) - 1;
+          b = b0 + l;
+          at += __shfl_sync(0xffffffffu, inc - c, l);
+          own = __shfl_sync(0xffffffffu, own, l);
+          break;
+        }
+        at += __shfl_sync(0xffffffffu, inc, 31);
+        b0 += 32;
+        if (b0 >= a.B) return false;   // not reached: th is the sum of these
       }
-      float *dst = kt + r * (D + 1);
-#pragma unroll
-      for (int u = 0; u < 16; ++u) dst[16 * g + u] = have ? v[u] : (u == 0 && g == 0 ? NAN : 0.f);
+      nt = own; wt = sc.wt;
+      const long long len = own_length(sc, own);
+      rt = (int)div64(y - at, len);
+      tile = y - at - rt * len - sc.ov;
+      unit = sc.rt_sh + b * sc.rt_own + rt;
+      unit_at = base + sh + at + rt * len;
     }
-    __syncthreads();
-    float x = 0.f;
-    const float *kr = kt + lane * (D + 1);
-#pragma unroll 8
-    for (int c = 0; c < D; ++c) x = fmaf(qs[warp * D + c], kr[c], x);
-    const bool ok = k0 + lane < total && kr[0] == kr[0];
-    x = ok ? x : -INFINITY;
-    float mx = x;
-    for (int w = 16; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-    const float mn = fmaxf(m, mx);
-    if (mn == -INFINITY) continue;
-    const float al = m == -INFINITY ? 0.f : expf(m - mn);
-    const float p = ok ? expf(x - mn) : 0.f;
-    float ps = p;
-    for (int w = 16; w > 0; w >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, w);
-    l = l * al + ps;
-    m = mn;
-#pragma unroll
-    for (int u = 0; u < D / 32; ++u) o[u] *= al;
-    for (int k = 0; k < kKeys; ++k) {
-      const float pk = __shfl_sync(0xffffffffu, p, k);
-      if (pk == 0.f) continue;
-#pragma unroll
-      for (int u = 0; u < D / 32; ++u) o[u] = fmaf(pk, kt[k * (D + 1) + lane + 32 * u], o[u]);
+    if (tile < 0) {    // in the unit's overhead: its first tile is the next position
+      *x -= tile;
+      continue;
     }
-  }
-  if (h < a.H) {
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-    for (int u = 0; u < D / 32; ++u) {
-      const __nv_bfloat16 v = __float2bfloat16_rn(o[u] * inv);
-      a.out[((size_t)row * a.H + h) * D + lane + 32 * u] = *reinterpret_cast<const uint16_t *>(&v);
+    if (tile > nt) {   // behind the start of the window's tiles: the window went with its first one
+      *x = unit_at + sc.ov + nt + wt;
+      continue;
     }
+    long long n = nt - tile;
+    if (n > x_end - *x) n = x_end - *x;
+    const bool win = wt > 0 && *x + (nt - tile) < x_end;
+    const long long done = win ? unit_at + sc.ov + nt + wt : *x + n;
+    if (lane == 0) {
+      const bool shared = unit < sc.rt_sh;
+      sg.half = half;
+      sg.b = b;
+      if (shared) {
+        const int rows = a.B * a.T_q * a.H;
+        sg.row0 = rt * kRows;
+        sg.nrows = rows - sg.row0 < kRows ? rows - sg.row0 : kRows;
+      } else {
+        const int rows = a.T_q * a.H;
+        sg.row0 = b * rows + rt * kRows;
+        sg.nrows = rows - rt * kRows < kRows ? rows - rt * kRows : kRows;
+      }
+      int ents = 0;
+      sg.seq = seq_entries(a, shared ? 0 : b, &ents);
+      sg.n_sink = 0;
+      sg.n_fp4 = (int)n;
+      sg.n_win = win ? 1 : 0;   // counted below
+      sg.key0 = (shared ? 0 : a.n_shared) + (int)tile * kTile;
+      sg.key_end = shared ? a.n_shared : ents;
+      const int u = half * sc.units + unit;
+      const int g0 = (int)div64(unit_at + sc.ov, chunk);
+      sg.slot = (int)blockIdx.x + u;
+      if (g0 == (int)blockIdx.x) {
+        const long long last = unit_at + sc.ov + (wt > 0 ? nt : nt - 1);
+        reinterpret_cast<int2 *>(a.ws)[u] = make_int2(g0 + u, (int)div64(last, chunk) - g0 + 1);
+      }
+    }
+    *x = done;
+    return true;
   }
-}
-
-template <int D>
-cudaError_t launch_simple(const DenseAttnArgs &a, cudaStream_t s) {
-  const size_t smem = (size_t)(kKeys * (D + 1) + kWarps * D) * 4;
-  cudaError_t e = cudaFuncSetAttribute(attn_dense_simple_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(attn_dense_simple_kernel<D>, dim3(a.B * a.T_q, (a.H + kWarps - 1) / kWarps), dim3(kWarps * 32), smem,
-                    s, dim3(1, 1, 1), a);
-}
-
-cudaError_t launch_simple_d(const DenseAttnArgs &a, cudaStream_t s) {
-  switch (a.D) {
-    case 128: return launch_simple<128>(a, s);
-    case 256: return launch_simple<256>(a, s);
-    default: return launch_simple<512>(a, s);
-  }
+  return false;
 }
 
 }  // namespace
 
-size_t prefix_attn_workspace_bytes(int, int, int, int, int) { return 0; }
+// MODE 0: prefix attention (paged entries and an optional window), partial
+// results; MODE 1: window with sinks, straight to the output.
+template <int D, int MODE>
+__global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const DenseAttnArgs a, const Schedule sc) {
+  using F = Cfg<D>;
+  constexpr int DO = F::DO, CS = F::CS, NCH = F::NCH, GC = F::GC, NG = F::NG, QT = F::QT, QS = F::QS;
+  constexpr uint32_t kIdS = mma_idesc(kRows, kTile, 0u, 0u);
+  constexpr uint32_t kIdO = mma_idesc(kRows, DO, 0u, 0u) | (1u << 16);   // B (V) MN-major
+  extern __shared__ uint8_t smem_raw[];
+  DenseSmem<D> &S = *reinterpret_cast<DenseSmem<D> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                     ~uintptr_t(1023));
+  volatile int *abort = &S.abort;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_launch_dependents();
+  if (tid == 0) {
+    for (int g = 0; g < NG; ++g) {
+      mbar_init(&S.full[g], kTeam);
+      mbar_init(&S.empty[g], 1);
+    }
+    for (int u = 0; u < kStages; ++u) {
+      mbar_init(&S.raw_full[u], 32);
+      mbar_init(&S.raw_empty[u], kTeam);
+    }
+    for (int u = 0; u < 2; ++u) {
+      mbar_init(&S.s_full[u], 1);
+      mbar_init(&S.p_full[u], 4);
+      mbar_init(&S.pv_done[u], 1);
+    }
+    mbar_init(&S.fin, 2);
+    S.abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&S.tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+  pdl_wait();
+
+  bool dead = false;
+  // A segment's start: the scheduler warp has written it (or that there is
+  // none).  Its Q in place (not for the scheduler, which writes the next one
+  // meanwhile, and the loader).  Its end: true when a wait of any role gave up.
+  uint32_t seg_i = 0;
+  auto begin_segment = [&]() -> bool {
+    named_bar(kSegBar, kThreads);
+    return S.more[seg_i & 1u] != 0;
+  };
+  auto q_in_place = [&]() { named_bar(kQBar, kThreads - 64); };
+  auto end_segment = [&]() -> bool {
+    ++seg_i;
+    return named_bar_or(kSegBar, kThreads, *abort != 0);
+  };
+  // Chunk of Q (64 channels) that S takes k-th: the other half's channels
+  // first.
+  auto q_chunk = [&](int k, int half) -> int { return CS > 1 ? (k + (half == 0 ? GC : 0)) % NCH : k; };
+  // bf16 -> fp16 with the sign of the softmax scale (so that the logits' own
+  // factor is not negative).
+  const float qsign = a.scale < 0.f ? -1.f : 1.f;
+  auto to_f16x2 = [&](uint32_t w) -> uint32_t {
+    const __half2 hv = __floats2half2_rn(bf16_to_f32(w & 0xFFFFu) * qsign, bf16_to_f32(w >> 16) * qsign);
+    return *reinterpret_cast<const uint32_t *>(&hv);
+  };
+  uint32_t gcount = 0, tcount = 0;   // ring groups and tiles so far (each role advances them alike)
+  uint32_t scount = 0;               // raw steps so far (load and dequantise)
+
+  if (warp < kDqWarps) {
+    // ================================================ fetch + dequantise
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFetch));
+    while (begin_segment()) {
+      const Segment &sg = S.seg[seg_i & 1u];
+      const int n_sink = sg.n_sink, n_fp4 = sg.n_fp4, n_tiles = n_sink + n_fp4 + sg.n_win;
+      const int half = sg.half;
+      // ---- Q's chunks of shared memory, rows behind the last one zero
+      if constexpr (QS > 0) {
+        const uint16_t *qrow = a.q + (size_t)sg.row0 * D;
+        const int nrows = sg.nrows;
+        constexpr int NP = kRows * QS * 8;   // 16-byte pieces
+#pragma unroll 1
+        for (int i0 = tid; i0 < NP; i0 += kDq * 8) {
+          uint4 v[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int i = i0 + u * kDq, r = i / (QS * 8), pc = i % (QS * 8);
+            v[u] = (i < NP && r < nrows)
+                       ? __ldg(reinterpret_cast<const uint4 *>(qrow + (size_t)r * D + q_chunk(QT + (pc >> 3), half) * 64) + (pc & 7))
+                       : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int i = i0 + u * kDq, r = i / (QS * 8), pc = i % (QS * 8);
+            if (i < NP)
+              *reinterpret_cast<uint4 *>(S.q + sw_off(r, pc, kRows)) =
+                  make_uint4(to_f16x2(v[u].x), to_f16x2(v[u].y), to_f16x2(v[u].z), to_f16x2(v[u].w));
+          }
+        }
+        fence_proxy_async();
+      }
+      q_in_place();
+      // ---- team t takes the groups whose running number is t modulo 2: the
+      // two halves of a tile's channels (D 512), or every other tile.  Lane =
+      // (row, 16-byte piece) so that the eight lanes of a store's phase meet
+      // eight different 16-byte columns of the swizzled rows
+      const uint32_t team = warp / kTeam;
+      const int p4 = (lane & 1) | ((lane >> 2) & 2);                                         // piece 0..3 (then 4..7)
+      const int r0 = (warp % kTeam) * 16 + ((lane >> 1) & 3) + ((lane >> 2) & 4);            // keys r0 and r0 + 8
+      auto hand_over = [&](uint64_t *bar) {   // generic stores -> visible to the tensor core
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+      };
+      auto all_wait = [&](uint64_t *bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort)) != 0;
+      };
+      constexpr int FP8_S = GC / 2;                        // steps of a group of FP8 rows
+      bool ok = true;
+#pragma unroll 1
+      for (int it = 0; it < n_tiles && ok; ++it) {
+        const bool fp4 = it >= n_sink && it < n_sink + n_fp4;
+        const uint32_t g_mine = CS > 1 ? team : 0u;
+        const bool mine = CS > 1 || (gcount & 1u) == team;
+        uint32_t step = scount + g_mine * (fp4 ? 1u : (uint32_t)FP8_S);
+        const uint32_t gi = gcount + g_mine;
+        gcount += CS;
+        scount += fp4 ? CS : CS * FP8_S;
+        if (!mine) continue;
+        const uint32_t slot = gi % NG, ph = (gi / NG) & 1u;
+        uint8_t *kv = S.kv[slot];
+        if (fp4) {
+          const uint32_t st = step % kStages;
+          ok = all_wait(&S.raw_full[st], (step / kStages) & 1u);
+          if (!ok) break;
+          constexpr int NU = GC / 2;                       // pieces of 32 channels per key
+          uint4 rv[NU][2];
+          uint32_t sb[NU][2];
+#pragma unroll
+          for (int u = 0; u < NU; ++u)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              rv[u][y] = *reinterpret_cast<const uint4 *>(S.raw[st] + raw_off(r0 + 8 * y, p4 + 4 * u));
+              sb[u][y] = *reinterpret_cast<const uint16_t *>(S.raw[st] + kRawSc + (r0 + 8 * y) * kRawScRow + (p4 + 4 * u) * 2);
+            }
+          __syncwarp();                                    // this warp's part of the stage is in registers
+          if (lane == 0) mbar_arrive(&S.raw_empty[st]);
+          ok = all_wait(&S.empty[slot], ph ^ 1u);
+          if (!ok) break;
+#pragma unroll
+          for (int u = 0; u < NU; ++u) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const uint32_t s0 = e4m3x2_to_f16x2(__byte_perm(sb[u][y], 0, 0x0000));
+              const uint32_t s1 = e4m3x2_to_f16x2(__byte_perm(sb[u][y], 0, 0x1111));
+              const uint32_t w[4] = {rv[u][y].x, rv[u][y].y, rv[u][y].z, rv[u][y].w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint32_t h[4];
+                e2m1x8_to_f16x2(w[j], h);
+                const __half2 sk = *reinterpret_cast<const __half2 *>(j < 2 ? &s0 : &s1);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const __half2 v = __hmul2(*reinterpret_cast<const __half2 *>(&h[e]), sk);
+                  h[e] = *reinterpret_cast<const uint32_t *>(&v);
+                }
+                *reinterpret_cast<uint4 *>(kv + sw_off(r0 + 8 * y, 4 * (p4 + 4 * u) + j, kTile)) =
+                    make_uint4(h[0], h[1], h[2], h[3]);
+              }
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int sub = 0; sub < FP8_S; ++sub, ++step) {  // two chunks a step
+            const uint32_t st = step % kStages;
+            ok = all_wait(&S.raw_full[st], (step / kStages) & 1u);
+            if (!ok) break;
+            uint4 rv[2][2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+                rv[u][y] = *reinterpret_cast<const uint4 *>(S.raw[st] + raw_off(r0 + 8 * y, p4 + 4 * u));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.raw_empty[st]);
+            if (sub == 0) ok = all_wait(&S.empty[slot], ph ^ 1u);
+            if (!ok) break;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {                  // 16 channels of chunk 2 sub + u
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                uint32_t h[8];
+                e4m3x4_to_f16x2(rv[u][y].x, h);
+                e4m3x4_to_f16x2(rv[u][y].y, h + 2);
+                e4m3x4_to_f16x2(rv[u][y].z, h + 4);
+                e4m3x4_to_f16x2(rv[u][y].w, h + 6);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  *reinterpret_cast<uint4 *>(kv + sw_off(r0 + 8 * y, 16 * sub + 8 * u + 2 * p4 + j, kTile)) =
+                      make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+              }
+            }
+          }
+          if (!ok) break;
+        }
+        hand_over(&S.full[slot]);
+      }
+      dead = end_segment();
+      if (dead) break;
+    }
+  } else if (warp < kSmWarp0 + 4) {
+    // ================================================ softmax: thread = row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    while (begin_segment()) {
+      const Segment &sg = S.seg[seg_i & 1u];
+      const int n_sink = sg.n_sink, n_fp4 = sg.n_fp4, n_tiles = n_sink + n_fp4 + sg.n_win;
+      const int half = sg.half;
+      const int q = warp & 3, row = 32 * q + lane;
+      const uint32_t lrow = tmem + ((uint32_t)(32 * q) << 16);
+      const int frow = sg.row0 + row;
+      const bool live = row < sg.nrows;
+      // ---- Q's first chunks: this thread's row into its tensor-memory lane
+      {
+        const uint4 *qp = reinterpret_cast<const uint4 *>(a.q + (size_t)frow * D);
+        uint4 v[QT][8];
+#pragma unroll
+        for (int k = 0; k < QT; ++k)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[k][i] = live ? __ldg(qp + q_chunk(k, half) * 8 + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < QT; ++k) {
+          uint32_t h[32];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            h[4 * i] = to_f16x2(v[k][i].x); h[4 * i + 1] = to_f16x2(v[k][i].y);
+            h[4 * i + 2] = to_f16x2(v[k][i].z); h[4 * i + 3] = to_f16x2(v[k][i].w);
+          }
+          tmem_st_x32(lrow + kColQ + 32 * k, h);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      q_in_place();
+      tc_fence_after();
+      const int t = live ? sg.pos[frow / a.H - sg.q0] : -1;
+      int vis = 0;                                 // entries this row sees
+      if (MODE == 0 && t >= 0) {
+        int n;
+        const int b = frow / (a.T_q * a.H);
+        if (seq_entries(a, b, &n) < 0) flag(a.status, CSA2_DEV_BAD_SEQUENCE);
+        const int v = (t + 1) / a.pool.m;
+        vis = n < v ? n : v;
+        if (vis > sg.key_end) vis = sg.key_end;
+      }
+      int wlo = t - a.window + 1;
+      if (wlo < 0) wlo = 0;
+      const int snk = MODE == 1 && t >= 0 ? (a.window > 0 ? wlo : t + 1) : 0;   // sinks below this token
+      auto warp_wait = [&](uint64_t *bar, uint32_t parity) {
+        int w_ok = 1;
+        if (lane == 0) w_ok = wait_or_abort(bar, parity, abort);
+        return __shfl_sync(0xffffffffu, w_ok, 0) != 0;
+      };
+      const int32_t *trow = sg.seq >= 0 ? a.pool.table + (size_t)sg.seq * a.pool.max_pages : nullptr;
+      // pages of FP4 tile f (lanes 0..4: at most 5 of 16 entries or more): the
+      // bytes of a slot without a page were never read, its keys are hidden
+      auto page_bad = [&](int f) -> bool {
+        const int e0 = sg.key0 + f * kTile;
+        int e1 = e0 + kTile;
+        if (e1 > sg.key_end) e1 = sg.key_end;
+        const int p = e0 / a.pool.page + lane;
+        if (f >= n_fp4 || (long long)p * a.pool.page >= e1) return false;
+        if (!trow) return true;
+        const int pg = __ldg(trow + p);
+        return pg < 0 || pg >= a.pool.n_pages;
+      };
+      float m_ref = -INFINITY, l = 0.f, vsc = 1.f;
+      bool bad_next = MODE == 0 && page_bad(0);
+      int wcur = 0;
+      bool ok = true;
+#pragma unroll 1
+      for (int it = 0; it < n_tiles; ++it) {
+        const uint32_t tc = tcount + it;
+        // the keys of this tile that this row sees: [ja, jb)
+        int ja = 0, jb;
+        float ksc = 1.f;
+        uint32_t badp = 0;
+        if (it < n_sink) {
+          jb = (snk < sg.key_end ? snk : sg.key_end) - it * kTile;
+          ksc = a.s_sink;
+        } else if (it < n_sink + n_fp4) {
+          jb = vis - (sg.key0 + (it - n_sink) * kTile);
+          badp = __ballot_sync(0xffffffffu, bad_next);
+          bad_next = page_bad(it - n_sink + 1);
+        } else {
+          int s = 0, e = 0;
+          next_window(sg, a.window, wcur, lane, &s, &e);
+          wcur = e;
+          ja = wlo - s;
+          jb = (t < e ? t + 1 : e) - s;
+          if (t < 0) jb = 0;
+          ksc = a.s_swa;
+        }
+        const bool whole = __all_sync(0xffffffffu, ja <= 0 && jb >= kTile) && badp == 0;
+        const uint32_t buf = tc & 1u, ph = (tc >> 1) & 1u;
+        const uint32_t scol = lrow + kColS + buf * kTile;
+        ok = warp_wait(&S.s_full[buf], ph);
+        if (!ok) break;
+        tc_fence_after();
+        // logits in base 2: lsc x S; never 0, so that a hidden key's -inf stays
+        const float lsc = fmaxf(fabsf(a.scale) * ksc * kLog2e, 1e-30f);
+        uint32_t sv[kTile];
+        tmem_ld_x32(scol, sv);
+        tmem_ld_x32(scol + 32, sv + 32);
+        tmem_wait_ld();
+        if (!whole) {
+          // bit j: key j is seen
+          const int lo = ja < 0 ? 0 : ja, hi = jb > kTile ? kTile : jb;
+          uint64_t seen = hi > lo ? (~0ull >> (kTile - (hi - lo))) << lo : 0ull;
+          if (badp) {   // rare
+            if (lane == 0) flag(a.status, CSA2_DEV_INDEX_RANGE);
+            const int e0 = sg.key0 + (it - n_sink) * kTile, p0 = e0 / a.pool.page;
+#pragma unroll 1
+            for (int j = 0; j < kTile; ++j)
+              if ((badp >> ((e0 + j) / a.pool.page - p0)) & 1u) seen &= ~(1ull << j);
+          }
+          const uint32_t s_lo = (uint32_t)seen, s_hi = (uint32_t)(seen >> 32);
+#pragma unroll
+          for (int j = 0; j < kTile; ++j)
+            if (!(((j < 32 ? s_lo : s_hi) >> (j & 31)) & 1u)) sv[j] = 0xFF800000u;
+        }
+        float mx4[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) mx4[u] = __uint_as_float(sv[u]);
+#pragma unroll
+        for (int j = 4; j < kTile; j += 8)
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            mx4[u] = j + 4 + u < kTile ? fmaxf(mx4[u], fmaxf(__uint_as_float(sv[j + u]), __uint_as_float(sv[j + 4 + u])))
+                                       : fmaxf(mx4[u], __uint_as_float(sv[j + u]));
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * lsc;
+        float al = 1.f;
+        if (mx > m_ref + kLazy || (m_ref == -INFINITY && mx != -INFINITY)) {
+          al = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - mx);
+          m_ref = mx;
+          l *= al;
+        }
+        const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+        uint32_t pr[kTile / 2];
+        {
+          const uint64_t l2 = f32x2(lsc, lsc), m2 = f32x2(-mu, -mu);
+          uint64_t ls0 = 0, ls1 = 0;
+#pragma unroll
+          for (int j = 0; j < kTile / 2; ++j) {
+            const float2 y = unpack_f32x2(fma_f32x2(f32x2(__uint_as_float(sv[2 * j]), __uint_as_float(sv[2 * j + 1])), l2, m2));
+            const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
+            if (j & 1) ls1 = add_f32x2(ls1, f32x2(p0, p1));
+            else ls0 = add_f32x2(ls0, f32x2(p0, p1));
+            const __half2 hv = __floats2half2_rn(p0, p1);
+            pr[j] = *reinterpret_cast<const uint32_t *>(&hv);
+          }
+          const float2 t2 = unpack_f32x2(add_f32x2(ls0, ls1));
+          l += t2.x + t2.y;
+        }
+        tmem_st_x32(scol, pr);   // this tile's S is in registers
+        // O moves with the reference maximum, and from one key scale to the next
+        const float conv = it > 0 && ksc != vsc ? vsc / ksc : 1.f;
+        const float f = al * conv;
+        if (it > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+          const uint32_t pt = tc - 1;                      // O of the tile before is complete
+          ok = warp_wait(&S.pv_done[pt & 1u], (pt >> 1) & 1u);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < DO; c += 32) {
+            uint32_t o[32];
+            tmem_ld_x32(lrow + kColO + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            tmem_st_x32(lrow + kColO + c, o);
+          }
+        }
+        vsc = ksc;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.p_full[buf]);
+      }
+      // ================================================ the segment's result
+      if (ok && n_tiles > 0) {
+        const uint32_t pt = tcount + n_tiles - 1;
+        ok = warp_wait(&S.pv_done[pt & 1u], (pt >> 1) & 1u);
+        tc_fence_after();
+      }
+      if (MODE == 1 && ok) {
+        const float inv = l > 0.f ? vsc / l : 0.f;
+        uint16_t *op = a.out + (size_t)frow * D + half * DO;
+#pragma unroll 1
+        for (int c = 0; c < DO; c += 32) {
+          uint32_t o[32];
+          if (n_tiles > 0) {
+            tmem_ld_x32(lrow + kColO + c, o);
+            tmem_wait_ld();
+          }
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float x0 = n_tiles > 0 ? __uint_as_float(o[2 * j]) * inv : 0.f;
+            const float x1 = n_tiles > 0 ? __uint_as_float(o[2 * j + 1]) * inv : 0.f;
+            const __nv_bfloat162 bv = __floats2bfloat162_rn(x0, x1);
+            pk[j] = *reinterpret_cast<const uint32_t *>(&bv);
+          }
+          if (live) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint4 *>(op + c + 8 * j) = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+          }
+        }
+      } else if (MODE == 0 && ok) {
+        const DenseWs w = dense_ws((long long)sc.units * CS, sc.grid, DO);
+        uint8_t *ws = static_cast<uint8_t *>(a.ws);
+        float2 *ml = reinterpret_cast<float2 *>(ws + w.off_ml) + (size_t)sg.slot * kRows;
+        float4 *po = reinterpret_cast<float4 *>(ws + w.off_o) + (size_t)sg.slot * (DO / 4) * kRows;
+        if (live) ml[row] = make_float2(m_ref, l);
+#pragma unroll 1
+        for (int c = 0; c < DO; c += 32) {
+          uint32_t o[32];
+          if (n_tiles > 0) {
+            tmem_ld_x32(lrow + kColO + c, o);
+            tmem_wait_ld();
+          }
+          if (live) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (n_tiles > 0)
+                v = make_float4(__uint_as_float(o[4 * j]) * vsc, __uint_as_float(o[4 * j + 1]) * vsc,
+                                __uint_as_float(o[4 * j + 2]) * vsc, __uint_as_float(o[4 * j + 3]) * vsc);
+              po[(size_t)(c / 4 + j) * kRows + row] = v;
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      tcount += n_tiles;
+      dead = end_segment();
+      if (dead) break;
+      tc_fence_after();
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
+    if (warp == kSchedWarp) {
+      // ================================================ scheduler: this block's share of the
+      // work is [x, x_end) of the tiles' linear order (prefix), every grid-th unit (window)
+      long long th = 0, chunk = 1, x, x_end;
+      if (MODE == 0) {
+        long long sum = 0;
+        for (int b = lane; b < a.B; b += 32) sum += own_length(sc, own_tiles(a, b));
+#pragma unroll 1
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        th = sc.rt_sh * shared_length(sc) + sc.rt_own * sum;
+        chunk = div64(th * CS + sc.grid - 1, sc.grid);
+        x = chunk * blockIdx.x;
+        x_end = x + chunk < th * CS ? x + chunk : th * CS;
+      } else {
+        x = blockIdx.x;
+        x_end = (long long)a.B * sc.rt_own * CS;
+      }
+      auto write_segment = [&](uint32_t i) -> bool {
+        Segment &sg = S.seg[i & 1u];
+        bool more;
+        if (MODE == 0) {
+          more = next_prefix_segment(a, sc, th, chunk, &x, x_end, lane, sg);
+        } else {
+          more = x < x_end;
+          if (more && lane == 0) {
+            const int half = (int)x % CS, u = (int)x / CS;
+            const int b = u / sc.rt_own, rt = u % sc.rt_own, rows = a.T_q * a.H;
+            sg.half = half; sg.b = b;
+            sg.row0 = b * rows + rt * kRows;
+            sg.nrows = rows - rt * kRows < kRows ? rows - rt * kRows : kRows;
+            sg.n_fp4 = 0; sg.key0 = 0; sg.key_end = 0; sg.seq = -1; sg.slot = -1;
+            sg.n_sink = 0;
+            sg.n_win = 1;
+          }
+          x += sc.grid;
+        }
+        __syncwarp();
+        if (more) {
+          const int q0 = sg.row0 / a.H, nq = (sg.row0 + sg.nrows - 1) / a.H - q0 + 1;
+          int top = -1;   // sinks end where the latest query's window starts
+          for (int i = lane; i < nq; i += 32) {
+            int t = a.q_pos[q0 + i];
+            if (t > kMaxPos) {   // sums with a tile or a window stay in 32 bits
+              flag(a.status, CSA2_DEV_BAD_POSITION);
+              t = -1;
+            }
+            sg.pos[i] = t;
+            if (t >= 0) {
+              int lo = a.window > 0 ? t - a.window + 1 : t + 1;
+              lo = lo < 0 ? 0 : lo;
+              top = lo > top ? lo : top;
+            }
+          }
+          top = __reduce_max_sync(0xffffffffu, top);
+          if (lane == 0) {
+            sg.q0 = q0;
+            sg.nq = nq;
+            if (MODE == 1) {
+              const int n = top < a.n_sink ? top : a.n_sink;
+              sg.key_end = n > 0 ? n : 0;
+              sg.n_sink = n > 0 ? (n + kTile - 1) / kTile : 0;
+            }
+          }
+          __syncwarp();
+          if (sg.n_win) {
+            int n = 0, cur = 0, s, e;
+            if (a.window > 0)
+              while (next_window(sg, a.window, cur, lane, &s, &e)) { ++n; cur = e; }
+            __syncwarp();
+            if (lane == 0) sg.n_win = n;
+          }
+        }
+        if (lane == 0) S.more[i & 1u] = more;
+        return more;
+      };
+      write_segment(0);
+      while (begin_segment()) {
+        write_segment(seg_i + 1);
+        dead = end_segment();
+        if (dead) break;
+      }
+    } else {
+    // ================================================ MMA issuer, loaders
+    while (begin_segment()) {
+      const Segment &sg = S.seg[seg_i & 1u];
+      const int n_sink = sg.n_sink, n_fp4 = sg.n_fp4, n_tiles = n_sink + n_fp4 + sg.n_win;
+      const int half = sg.half;
+      if (warp != kLoadWarp) q_in_place();   // (the loader does not need it)
+      if (warp == kMmaWarp) {
+        // One elected lane runs the whole loop, its waits included: measured, a
+        // converged warp that elects a lane per group of MMAs issues the S
+        // product at 59 cycles per MMA even with nothing else on the SM (130 in
+        // this kernel), one lane at the tensor core's own 38.
+        if (elect_one()) {
+          tc_fence_after();
+          const uint64_t dq0 = smem_desc_kmajor(smem_u32(S.q), 128);
+          bool ok = true;
+#pragma unroll 1
+          for (int it = 0; it < n_tiles && ok; ++it) {
+            // the buffer's last P has been used; both barriers are asked before
+            // either answer is needed (a wait behind issued MMAs costs about
+            // 150 cycles, ready or not)
+            const uint32_t tc = tcount + it, buf = tc & 1u, pp = ((tc >> 1) & 1u) ^ 1u;
+            const uint32_t scol = tmem + kColS + buf * kTile;
+            uint32_t slot = gcount % NG, ph = (gcount / NG) & 1u;
+            const bool r0 = tc < 2 || mbar_test_wait(&S.pv_done[buf], pp);
+            const bool r1 = mbar_test_wait(&S.full[slot], ph);
+            if (!r0) ok = wait_or_abort(&S.pv_done[buf], pp, abort);
+            if (ok && !r1) ok = wait_or_abort(&S.full[slot], ph, abort);
+            if (!ok) break;
+#pragma unroll
+            for (int g = 0; g < CS; ++g) {   // groups of chunks in S's order, straight-line code
+              if (g > 0) {
+                slot = gcount % NG;
+                ph = (gcount / NG) & 1u;
+                ok = wait_or_abort(&S.full[slot], ph, abort);
+                if (!ok) break;
+              }
+              ++gcount;
+              tc_fence_after();
+              const uint64_t db = smem_desc_kmajor(smem_u32(S.kv[slot]), 128);
+#pragma unroll
+              for (int c = 0; c < GC; ++c) {
+                const int k = g * GC + c;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                  const uint64_t bd = db + (uint64_t)((c * (kTile * 128) + kk * 32) >> 4);
+                  if (k < QT)
+                    tc_mma_f16_ta(scol, tmem + kColQ + 32 * k + 8 * kk, bd, kIdS, (k > 0 || kk > 0) ? 1u : 0u);
+                  else
+                    tc_mma_f16(scol, dq0 + (uint64_t)(((k - QT) * (kRows * 128) + kk * 32) >> 4), bd, kIdS, 1u);
+                }
+              }
+              if (CS > 1 && g == 0) tc_commit(&S.empty[slot]);   // the other half's channels: only S needs them
+            }
+            if (!ok) break;
+            tc_commit(&S.s_full[buf]);
+          }
+        }
+        __syncwarp();
+      } else if (warp == kPvWarp) {
+        if (elect_one()) {
+#pragma unroll 1
+          for (int it = 0; it < n_tiles; ++it) {
+            const uint32_t slot = (gcount + CS - 1) % NG;   // the tile's group of this block's channels
+            gcount += CS;
+            const uint32_t tc = tcount + it, buf = tc & 1u;
+            if (!wait_or_abort(&S.p_full[buf], (tc >> 1) & 1u, abort)) break;
+            tc_fence_after();
+            const uint64_t dv = smem_desc_mnmajor_sw128(smem_u32(S.kv[slot]), kTile * 128, 1024);
+#pragma unroll
+            for (int ks = 0; ks < kTile / 16; ++ks)
+              tc_mma_f16_ta(tmem + kColO, tmem + kColS + buf * kTile + ks * 8, dv + ((2 * ks * 1024) >> 4), kIdO,
+                            (it > 0 || ks > 0) ? 1u : 0u);
+            tc_commit(&S.empty[slot]);
+            tc_commit(&S.pv_done[buf]);
+          }
+        }
+        __syncwarp();
+      } else if (warp == kLoadWarp) {
+        // ---- the raw steps: lane = key r of the tile for its address; a copy's
+        // lanes lie along the rows (a row's 256 bytes by 16 lanes)
+        const int page = a.pool.page > 0 ? a.pool.page : 1;
+        const int32_t *trow = sg.seq >= 0 ? a.pool.table + (size_t)sg.seq * a.pool.max_pages : nullptr;
+        // FP4: places of the lane's two keys in the page list, advanced tile by
+        // tile; their pages are looked up a tile ahead
+        const int adv_p = kTile / page, adv_o = kTile % page;
+        int e_cur = sg.key0 + lane, left = n_fp4;
+        int p_idx[2] = {e_cur / page, (e_cur + 32) / page}, p_off[2] = {e_cur % page, (e_cur + 32) % page}, pg_next[2];
+        auto page_of = [&](int y) -> int {
+          return left > 0 && trow && e_cur + 32 * y < sg.key_end ? __ldg(trow + p_idx[y]) : -1;
+        };
+        pg_next[0] = page_of(0);
+        pg_next[1] = page_of(1);
+        int wcur = 0;
+        bool ok = true;
+        auto acquire = [&](uint32_t st) {
+          return __all_sync(0xffffffffu, wait_or_abort(&S.raw_empty[st], ((scount / kStages) & 1u) ^ 1u, abort)) != 0;
+        };
+        // 32 rows from row0 on of stage st: LPR lanes of 16 bytes per row; p: the
+        // address of this lane's key, nullptr = zeros
+        auto copy_rows = [&](uint32_t st, int row0, const uint8_t *p, auto lpr) {
+          constexpr int LPR = decltype(lpr)::value, RPI = 32 / LPR;
+          const unsigned long long mine = reinterpret_cast<unsigned long long>(p);
+          const uint8_t *any = a.pool.codes ? a.pool.codes : (a.swa_rows ? a.swa_rows : a.sink_rows);
+          const uint32_t dst = smem_u32(S.raw[st]);
+#pragma unroll
+          for (int i = 0; i < LPR; ++i) {
+            const int row = i * RPI + lane / LPR, pc = lane % LPR;
+            const uint8_t *src = reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, mine, row));
+            cp_async<16>(dst + raw_off(row0 + row, pc), src ? src + pc * 16 : any, src != nullptr);
+          }
+        };
+#pragma unroll 1
+        for (int it = 0; it < n_tiles && ok; ++it) {
+          if (it >= n_sink && it < n_sink + n_fp4) {
+            size_t er[2];
+            bool have[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              have[y] = pg_next[y] >= 0 && pg_next[y] < a.pool.n_pages;
+              er[y] = have[y] ? (size_t)pg_next[y] * page + p_off[y] : 0;
+              p_idx[y] += adv_p;
+              p_off[y] += adv_o;
+              if (p_off[y] >= page) { p_off[y] -= page; ++p_idx[y]; }
+            }
+            --left;
+            e_cur += kTile;
+            pg_next[0] = page_of(0);
+            pg_next[1] = page_of(1);
+#pragma unroll 1
+            for (int g = 0; g < CS; ++g) {
+              const uint32_t st = scount % kStages;
+              ok = acquire(st);
+              if (!ok) break;
+              const int c0 = q_chunk(g * GC, half);
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                copy_rows(st, 32 * y, have[y] ? a.pool.codes + er[y] * (D / 2) + c0 * 32 : nullptr, Int<GC * 2>{});
+                constexpr int SB = GC * 4;   // scale bytes of a key in a step
+                cp_async<SB>(smem_u32(S.raw[st]) + kRawSc + (32 * y + lane) * kRawScRow,
+                             a.pool.scales + er[y] * (D / 16) + c0 * 4, have[y]);
+              }
+              cp_async_arrive(&S.raw_full[st]);
+              ++scount;
+            }
+          } else {
+            const uint8_t *row[2] = {nullptr, nullptr};
+            if (it < n_sink) {
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const int key = it * kTile + 32 * y + lane;
+                if (key < sg.key_end) row[y] = a.sink_rows + ((size_t)sg.b * a.sink_cap + key) * D;
+              }
+            } else {
+              int s = 0, e = 0;
+              next_window(sg, a.window, wcur, lane, &s, &e);
+              wcur = e;
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                const int tok = s + 32 * y + lane;
+                if (tok < e) row[y] = a.swa_rows + ((size_t)sg.b * a.W_cap + tok % a.W_cap) * D;
+              }
+            }
+#pragma unroll 1
+            for (int k = 0; k < NCH; k += 2) {   // two chunks a step, in S's order
+              const uint32_t st = scount % kStages;
+              ok = acquire(st);
+              if (!ok) break;
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+                copy_rows(st, 32 * y, row[y] ? row[y] + q_chunk(k, half) * 64 : nullptr, Int<8>{});
+              cp_async_arrive(&S.raw_full[st]);
+              ++scount;
+            }
+          }
+        }
+        cp_async_wait_all();   // none in flight when the segment (or, after a wait that gave up, the block) ends
+      }
+      tcount += n_tiles;
+      dead = end_segment();
+      if (dead) break;
+    }
+    }
+  }
+  if (dead) {
+    if (tid == 0) flag(a.status, CSA2_DEV_TIMEOUT);
+    if (warp == kMmaWarp || warp == kPvWarp) {   // every MMA issued so far is done before its memory goes
+      if (elect_one()) {
+        tc_commit(&S.fin);
+        mbar_wait_bounded(&S.fin, 0, kWaitLimit);
+      }
+      __syncwarp();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Joins the parts of every row: out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.
+// Block: a row tile of 128 flattened rows x 8 channels; thread = (row, share of
+// the parts), so that a row's parts are in flight together; the parts' planes
+// are [channel / 4][row], so every load is coalesced.
+constexpr int kMergeShares = 4, kMergeCh = 8;
+template <int D>
+__global__ void __launch_bounds__(kRows * kMergeShares) attn_dense_merge_kernel(const DenseAttnArgs a, const Schedule sc) {
+  using F = Cfg<D>;
+  constexpr int DO = F::DO;
+  __shared__ float red[kMergeShares][kRows];
+  __shared__ float4 racc[kMergeShares - 1][kMergeCh / 4][kRows];
+  const int row = threadIdx.x % kRows, share = threadIdx.x / kRows;
+  pdl_launch_dependents();
+  pdl_wait();
+  const long long rows = (long long)a.B * a.T_q * a.H;
+  const long long frow = (long long)blockIdx.x * kRows + row;
+  const bool live = frow < rows;
+  const int ch0 = blockIdx.y * kMergeCh, half = ch0 / DO, c0 = ch0 % DO;
+  const int b = live ? (int)(frow / ((long long)a.T_q * a.H)) : 0;
+  const int orow = live ? (int)(frow - (long long)b * a.T_q * a.H) : 0;
+  const DenseWs w = dense_ws((long long)sc.units * F::CS, sc.grid, DO);
+  const uint8_t *ws = static_cast<const uint8_t *>(a.ws);
+  const int2 *desc = reinterpret_cast<const int2 *>(ws) + (size_t)half * sc.units;
+  const float2 *ml = reinterpret_cast<const float2 *>(ws + w.off_ml);
+  const float4 *po = reinterpret_cast<const float4 *>(ws + w.off_o);
+  int2 sh = make_int2(0, 0), ow = make_int2(0, 0);   // (first slot, slots) of the prefix and of the row's own keys
+  if (live && sc.nt_sh > 0) sh = __ldcg(desc + blockIdx.x);
+  if (live && own_tiles(a, b) + sc.wt > 0) ow = __ldcg(desc + sc.rt_sh + b * sc.rt_own + orow / kRows);
+  const int parts = sh.y + ow.y;
+  auto place = [&](int s) -> size_t {   // part s: slot * 128 + row of the slot
+    return s < sh.y ? (size_t)(sh.x + s) * kRows + row : (size_t)(ow.x + s - sh.y) * kRows + orow % kRows;
+  };
+  float M = -INFINITY;
+#pragma unroll 4
+  for (int s = share; s < parts; s += kMergeShares) M = fmaxf(M, __ldcg(&ml[place(s)]).x);
+  red[share][row] = M;
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < kMergeShares; ++u) M = fmaxf(M, red[u][row]);
+  const float Mu = M == -INFINITY ? 0.f : M;
+  float4 acc[kMergeCh / 4];
+#pragma unroll
+  for (int j = 0; j < kMergeCh / 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float L = 0.f;
+#pragma unroll 4
+  for (int s = share; s < parts; s += kMergeShares) {
+    const size_t at = place(s), slot = at / kRows, r = at % kRows;
+    const float2 v = __ldcg(&ml[at]);
+    const float4 *p = po + (slot * (DO / 4) + c0 / 4) * kRows + r;
+    float4 o[kMergeCh / 4];
+#pragma unroll
+    for (int j = 0; j < kMergeCh / 4; ++j) o[j] = __ldcg(p + (size_t)j * kRows);
+    const float f = exp2f(v.x - Mu);
+    L = fmaf(f, v.y, L);
+#pragma unroll
+    for (int j = 0; j < kMergeCh / 4; ++j) {
+      acc[j].x = fmaf(f, o[j].x, acc[j].x);
+      acc[j].y = fmaf(f, o[j].y, acc[j].y);
+      acc[j].z = fmaf(f, o[j].z, acc[j].z);
+      acc[j].w = fmaf(f, o[j].w, acc[j].w);
+    }
+  }
+  __syncthreads();   // red is read
+  red[share][row] = L;
+  if (share > 0) {
+#pragma unroll
+    for (int j = 0; j < kMergeCh / 4; ++j) racc[share - 1][j][row] = acc[j];
+  }
+  __syncthreads();
+  if (share > 0 || !live) return;
+  L = 0.f;
+#pragma unroll
+  for (int u = 0; u < kMergeShares; ++u) L += red[u][row];
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  uint32_t pk[kMergeCh / 2];
+#pragma unroll
+  for (int j = 0; j < kMergeCh / 4; ++j) {
+#pragma unroll
+    for (int u = 0; u < kMergeShares - 1; ++u) {
+      const float4 v = racc[u][j][row];
+      acc[j].x += v.x; acc[j].y += v.y; acc[j].z += v.z; acc[j].w += v.w;
+    }
+    const __nv_bfloat162 x = __floats2bfloat162_rn(acc[j].x * inv, acc[j].y * inv);
+    const __nv_bfloat162 y = __floats2bfloat162_rn(acc[j].z * inv, acc[j].w * inv);
+    pk[2 * j] = *reinterpret_cast<const uint32_t *>(&x);
+    pk[2 * j + 1] = *reinterpret_cast<const uint32_t *>(&y);
+  }
+  *reinterpret_cast<uint4 *>(a.out + frow * D + ch0) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+}
+
+namespace {
+
+long long prefix_units(int B, int T_q, int H, int D) {
+  const long long rows = (long long)B * T_q * H;
+  const int cs = D > 256 ? D / 256 : 1;
+  return cs * ((rows + kRows - 1) / kRows + (long long)B * ((T_q * H + kRows - 1) / kRows));
+}
+
+template <int D, int MODE>
+cudaError_t launch_dense(const DenseAttnArgs &a, const Schedule &sc, cudaStream_t s) {
+  const size_t smem = sizeof(DenseSmem<D>) + 1024;
+  static_assert(sizeof(DenseSmem<D>) + 1024 <= 232448, "shared memory");
+  cudaError_t e = cudaFuncSetAttribute(attn_dense_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attn_dense_kernel<D, MODE>, dim3(sc.grid), dim3(kThreads), smem, s, dim3(1, 1, 1), a, sc);
+}
+
+template <int D>
+cudaError_t launch_prefix_t(const DenseAttnArgs &a, int sms, cudaStream_t s) {
+  const Schedule sc = make_schedule(a, Cfg<D>::CS, sms);
+  cudaError_t e = launch_dense<D, 0>(a, sc, s);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attn_dense_merge_kernel<D>, dim3(sc.rt_sh, D / kMergeCh), dim3(kRows * kMergeShares), 0, s, dim3(1, 1, 1), a, sc);
+}
+
+template <int D>
+cudaError_t launch_window_t(const DenseAttnArgs &a, int sms, cudaStream_t s) {
+  Schedule sc = make_schedule(a, Cfg<D>::CS, sms);
+  const long long units = (long long)a.B * sc.rt_own * Cfg<D>::CS;
+  if (units < sc.grid) sc.grid = (int)units;
+  return launch_dense<D, 1>(a, sc, s);
+}
+
+}  // namespace
+
+size_t prefix_attn_workspace_bytes(int B, int T_q, int H, int D, int sms) {
+  return dense_ws(prefix_units(B, T_q, H, D), sms, D < 256 ? D : 256).bytes;
+}
+cudaError_t launch_prefix_attn(const DenseAttnArgs &a, int sms, cudaStream_t s) {
+  switch (a.D) {
+    case 128: return launch_prefix_t<128>(a, sms, s);
+    case 256: return launch_prefix_t<256>(a, sms, s);
+    default: return launch_prefix_t<512>(a, sms, s);
+  }
+}
 size_t window_attn_workspace_bytes(int, int, int, int, int, int, int) { return 0; }
-cudaError_t launch_prefix_attn(const DenseAttnArgs &a, int, cudaStream_t s) { return launch_simple_d(a, s); }
-cudaError_t launch_window_attn(const DenseAttnArgs &a, int, cudaStream_t s) { return launch_simple_d(a, s); }
+cudaError_t launch_window_attn(const DenseAttnArgs &a, int sms, cudaStream_t s) {
+  switch (a.D) {
+    case 128: return launch_window_t<128>(a, sms, s);
+    case 256: return launch_window_t<256>(a, sms, s);
+    default: return launch_window_t<512>(a, sms, s);
+  }
+}
 
 }  // namespace csa2

@@ -387,7 +387,7 @@ CSA2_API csa2_status csa2_topk_noalloc(const float *scores, int rows, int64_t ld
  * An empty pool is refs = 0, table = -1, n_entries = 0.
  * m: tokens per entry, 1 or 2 (only the attention's visibility uses it).
  * Supported: D in {128, 256, 512}; page a multiple of 16 in [16, 4096];
- * n_pages * page < 2^31.
+ * n_pages * page < 2^31; max_pages * page <= 2^30.
  */
 typedef struct {
     uint8_t *codes;
@@ -451,15 +451,17 @@ CSA2_API csa2_status csa2_pages_compact(const csa2_page_pool *pool, int32_t *n_l
  *     once for the whole batch.
  *  pool   the entries; seq [B] i32 DEVICE: pool sequence of each batch row
  *  n_shared (host) entries that the batch's sequences have in common: they are
- *         read once, through the table of seq[0] (0 = nothing is shared).
- *         That the sequences agree on them is the caller's word; a sequence
- *         with fewer entries sees only its own number of them.
+ *         read once, through the table of seq[0], which holds them all (0 =
+ *         nothing is shared).  That the sequences agree on them is the
+ *         caller's word; a sequence with fewer entries sees only its own
+ *         number of them.
  *  swa    window cache of the layer with B rows (NULL: no window)
  *  q      [B][T_q][H][D] bf16, q_pos [B][T_q] i32 token position t of each query
  *  out    [B][T_q][H][D] bf16: softmax over the entries e < min(n_entries,
  *         floor((t+1)/m)) of the sequence and the window rows of tokens
  *         max(0,t-window+1)..t, of scale * q . x^, FP32 accumulation; zeros
- *         when that set is empty (a padded query: t = -1)
+ *         when that set is empty (a padded query: t = -1; t above 2^31 - 4,097 is
+ *         taken as -1, CSA2_DEV_BAD_POSITION)
  *  ws, ws_bytes: csa2_prefix_attn_workspace_size(B, T_q, H, D) bytes
  * |q| must be below 65,504 (the products run in fp16).
  * Supported: 1 <= H <= 64, B * T_q <= 65,535, window <= 1024.
@@ -482,7 +484,8 @@ CSA2_API size_t csa2_prefix_attn_workspace_size(int B, int T_q, int H, int D);
  *  q, q_pos, out as for entry 10; a query at t sees the tokens
  *         max(0,t-window+1)..t and the sinks before them (no token twice)
  *  ws, ws_bytes: csa2_window_attn_workspace_size(...) bytes
- * |q| must be below 65,504.  Supported: as for entry 10.
+ * |q| must be below 65,504.
+ * Supported: 1 <= H <= 64, B * T_q <= 2^22, window <= 1024, at most 1024 sinks.
  */
 CSA2_API csa2_status csa2_window_attn(const csa2_swa_cache *swa, const csa2_swa_cache *sinks, const uint16_t *q,
                                       const int32_t *q_pos, int T_q, int H, float softmax_scale, uint16_t *out,

@@ -531,6 +531,17 @@ def test_window_attention_without_a_window_sees_its_sinks():
     run_window(2, 3, 8, 256, 0, 9, 4, seed=3)
 
 
+def test_window_attention_of_more_queries_than_16_bits_count():
+    # one visible key a query: the output is its row
+    T, D = 70001, 128
+    rows = e4m3_rows(gen(6), 1, T, D)
+    q = torch.randn(1, T, 1, D, generator=gen(7), device="cuda").to(torch.bfloat16)
+    out = torch.empty_like(q)
+    C.csa2_window_attn(C.SwaCache.of(rows, scale=0.5, window=1), None, q, i32(range(T)).view(1, T), 0.1, out)
+    ref = (rows[0].view(torch.float8_e4m3fn).float() * 0.5).to(torch.bfloat16)
+    assert torch.equal(out[0, :, 0], ref) and C.csa2_device_status() == 0
+
+
 def test_window_attention_large_logits():
     run_window(1, 40, 64, 512, 128, 4, 400, seed=4, spread=6.0, scale=0.4)
     run_window(1, 40, 16, 128, 700, 4, 900, seed=5, spread=6.0, scale=0.7)
