@@ -44,9 +44,7 @@
 // at named barriers, so that the registers can be divided between the roles.
 // Every wait is bounded: one that gives up flags the device status and stops
 // every role; issued MMAs are drained and TMEM freed before the block exits.
-#include <limits.h>
-
-#include "common.cuh"
+#include "attn_dense.cuh"
 #include "kernels.h"
 
 namespace csa2 {
@@ -70,13 +68,8 @@ constexpr int kPvWarp = 14;                  // MMA issuer of O (kMmaWarp: of S)
 constexpr int kStages = 3;                   // raw steps in flight or in use
 // A stage: 64 rows of 128 bytes (codes, or FP8 values), then 64 x 16 of scales.
 constexpr int kRawRow = 128, kRawSc = kTile * kRawRow, kRawScRow = 16, kRawBytes = kRawSc + kTile * kRawScRow;
-constexpr int kRows = 128;                   // rows per unit
 constexpr int kUnitCost = 5;                 // see Schedule::ov: 12k cycles at 2.7k a tile (D 512)
-constexpr int kMaxQ = kRows + 1;             // queries that 128 rows can touch
-constexpr int kMaxPos = INT_MAX - 4096;
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 15.0f;               // log2 headroom of P below fp16's 65,504
-constexpr uint32_t kWaitLimit = 1u << 22;
 // TMEM columns: O, S of two tiles (each later its P), Q's first chunks
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 384, kTmemCols = 512;
 
@@ -126,20 +119,10 @@ struct DenseSmem {
   Segment seg[2];                                                                // this one and the next
 };
 
-__device__ __forceinline__ uint32_t sw_off(int r, int pc, int rows) {   // 16-byte piece pc of row r
-  return (uint32_t)((pc >> 3) * rows * 128 + r * 128 + (((pc & 7) ^ (r & 7)) << 4));
-}
-
 // Place of 16-byte piece pc of row r in a raw stage: eight lanes that read 4
 // rows x 2 neighbouring pieces meet eight different columns.
 __device__ __forceinline__ uint32_t raw_off(int r, int pc) {
   return (uint32_t)(r * kRawRow + ((pc ^ ((r & 3) << 1)) << 4));
-}
-
-__device__ __forceinline__ float ex2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 // Asynchronous copies to shared memory; `live` false writes zeros instead.
@@ -158,37 +141,6 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void mbar_arrive_n(uint64_t *bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
-}
-
-// Two fp32 operations per instruction.
-__device__ __forceinline__ uint64_t f32x2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 unpack_f32x2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
-__device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, volatile int *abort) {
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 255u) == 255u && *abort) return false;
-  }
-  *abort = 1;
-  return false;
 }
 
 // The next stretch of at most 64 window tokens at or behind `cur` that the
@@ -1264,6 +1216,7 @@ cudaError_t launch_prefix_attn(const DenseAttnArgs &a, int sms, cudaStream_t s) 
 }
 size_t window_attn_workspace_bytes(int, int, int, int, int, int, int) { return 0; }
 cudaError_t launch_window_attn(const DenseAttnArgs &a, int sms, cudaStream_t s) {
+  if (window_fits_ring(a)) return launch_window_ring(a, sms, s);
   switch (a.D) {
     case 128: return launch_window_t<128>(a, sms, s);
     case 256: return launch_window_t<256>(a, sms, s);

@@ -1,0 +1,611 @@
+// Sliding-window attention with sinks, resident form: windows whose rows, for
+// all the queries of 128 flattened (query, head) rows, fit shared memory.
+// DeepSeek-V4.1-Flash (jaehun.me review), "새로운 접근법" and its flowchart:
+// layers 1-2 use sliding-window attention only.
+//   out = sum_k softmax_k(scale q . x_k) x_k over the window's tokens and the
+//   first tokens before it, K = V shared by the heads.
+//
+// A block walks over consecutive row tiles of a sequence and keeps the window's
+// rows as an fp16 ring in shared memory (slot = token mod ring size; the order
+// of keys does not matter, a row's visible slots are a bit mask), so each window
+// row is fetched and converted once per block, not once per query.  All keys of
+// a tile are in one S = Q K^T (M 128, N = ring), so the softmax needs no running
+// maximum and O no rescaling: O = P V is formed 64 channels at a time in a
+// three-deep ring of tensor-memory columns and stored as it is formed.  What is
+// left is the traffic of q and the output, 4 bytes per (row, channel), which
+// bounds the kernel (132 FLOP per byte at a window of 128 and D 512).
+// Warp roles, all persistent, handing work over through mbarriers:
+//   warps 0-7    new window rows (E4M3 -> fp16), then Q (bf16 -> fp16) chunk by
+//                chunk (64 channels) into a ring of A operands, the next chunk's
+//                loads in flight
+//   warps 8-11   softmax, one row per thread; P replaces S in tensor memory
+//   warp 12, 14  tcgen05.mma issuers of S and of O (one lane each)
+//   warp 15      scheduler: passes (below) through a ring of three descriptors
+//   warps 16-19  O / l -> bf16 -> output, through a per-warp staging tile so that
+//                whole sectors are stored
+// A pass is a row tile with the range of tokens it needs; a tile whose queries'
+// windows do not fit one range (positions far apart) takes several passes, each
+// storing the rows it covers.  Sinks and window rows enter unscaled; with y =
+// log2 of a weight times its key's scale, P = 2^(y - max y) and the sum of the
+// weights is sum(P of sinks) / s_sink + sum(P of window) / s_window.
+// Every wait is bounded: one that gives up flags the device status and stops
+// every role; issued MMAs are drained and TMEM freed before the block exits.
+#include "attn_dense.cuh"
+#include "kernels.h"
+
+namespace csa2 {
+
+namespace {
+
+constexpr int kLdWarps = 8;                  // window rows and Q
+constexpr int kSmWarp0 = 8, kMmaWarp = 12, kPvWarp = 14, kSchedWarp = 15, kEpiWarp0 = 16;
+constexpr int kThreads = 20 * 32;
+constexpr int kLd = kLdWarps * 32;
+// Registers per thread of the five warpgroups (2 x load, softmax, MMA, output);
+// their sum is at most the launch's 5 x 96.
+constexpr int kRegsLoad = 96, kRegsSoftmax = 112, kRegsMma = 72, kRegsEpi = 104;
+constexpr int kPasses = 3;                   // descriptors
+constexpr int kQSlots = 4;                   // ring of Q chunks (so the loaders are at most three passes ahead of S)
+constexpr int kOBufs = 3;                    // ring of 64-channel O blocks
+constexpr int kLive = 8;                     // passes that can be unfinished at once (bounded by the rings above)
+constexpr uint32_t kTmemCols = 512;
+
+// Keys that the ring holds (N of S): 144 KB at D 512.
+__host__ __device__ constexpr int ring_keys(int D) { return D == 512 ? 144 : 160; }
+
+struct Pass {
+  int more;                // 0: no further pass
+  int row0, nrows, b;
+  int q0, nq;
+  int lo, end;             // tokens [lo, end) that the covered queries see (none: end <= lo)
+  int from;                // queries before this token were covered by an earlier pass of the tile
+  int first;               // first pass of the tile (it also covers padded queries)
+  int load_lo;             // window rows [load_lo, end) enter the ring
+  int load_sinks;          // a new sequence: its sinks enter too
+  int wait_for;            // passes that must be complete before the rows enter
+  int pos[kMaxQ];
+};
+
+template <int D>
+struct WinSmem {
+  static constexpr int R = ring_keys(D);
+  alignas(1024) uint8_t kr[(D / 64) * R * 128];     // ring: chunks of [R keys x 128 B]
+  alignas(1024) uint8_t q[kQSlots][kRows * 128];    // Q chunks
+  alignas(16) uint8_t stage[4][32 * 64];            // per output warp: 32 rows x 32 channels bf16
+  float linv[4][kRows];                             // 1 / l of a pass's rows, negative: not covered
+  uint64_t q_full[kQSlots], q_empty[kQSlots], k_full[4], s_full[2], p_full[2], pv_done[2];
+  uint64_t o_full[kOBufs], o_empty[kOBufs], pass_full[kPasses], pass_empty[kPasses], fin;
+  uint32_t tmem_base;
+  int abort;
+  int passes_done;                                  // complete O products
+  Pass pass[kPasses];
+};
+
+// TMEM columns: S of two passes (each later its P), then the O ring
+constexpr uint32_t kSCols = 160, kColS = 0, kColO = 2 * kSCols;
+static_assert(kColO + kOBufs * 64 <= kTmemCols, "tensor memory");
+
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// E4M3 bytes with the NaN codes (0x7F, 0xFF) made zero: rows between two
+// queries' windows may never have been written.
+__device__ __forceinline__ uint32_t no_nan(uint32_t w) {
+  const uint32_t m = (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7;
+  return w & ~(m * 0xFFu);
+}
+
+}  // namespace
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAttnArgs a, const int rt_own) {
+  constexpr int R = ring_keys(D), NCH = D / 64;
+  constexpr uint32_t kIdS = mma_idesc(kRows, R, 0u, 0u);
+  constexpr uint32_t kIdO = mma_idesc(kRows, 64, 0u, 0u) | (1u << 16);   // B (V) MN-major
+  extern __shared__ uint8_t smem_raw[];
+  WinSmem<D> &S = *reinterpret_cast<WinSmem<D> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  volatile int *abort = &S.abort;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n_sink = a.n_sink, rw = R - n_sink > 0 ? R - n_sink : 1;   // ring: slots [0, n_sink) sinks, then token mod rw
+  pdl_launch_dependents();
+  if (tid == 0) {
+    for (int i = 0; i < kQSlots; ++i) { mbar_init(&S.q_full[i], kLdWarps); mbar_init(&S.q_empty[i], 1); }
+    for (int i = 0; i < 4; ++i) mbar_init(&S.k_full[i], kLdWarps);
+    for (int i = 0; i < 2; ++i) { mbar_init(&S.s_full[i], 1); mbar_init(&S.p_full[i], 4); mbar_init(&S.pv_done[i], 1); }
+    for (int i = 0; i < kOBufs; ++i) { mbar_init(&S.o_full[i], 1); mbar_init(&S.o_empty[i], 4); }
+    for (int i = 0; i < kPasses; ++i) { mbar_init(&S.pass_full[i], 1); mbar_init(&S.pass_empty[i], kLdWarps + 4 + 4 + 2); }
+    mbar_init(&S.fin, 2);
+    S.abort = 0;
+    S.passes_done = 0;
+    fence_barrier_init();
+  }
+  // slots that no row has entered hold zeros
+  for (int i = tid; i < NCH * R * 8; i += kThreads) reinterpret_cast<uint4 *>(S.kr)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async();
+  if (warp == kMmaWarp) {
+    tmem_alloc(&S.tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+  pdl_wait();
+
+  // this pass's descriptor; every role takes all passes in order
+  uint32_t pi = 0;
+  auto next_pass = [&]() -> bool {
+    return __all_sync(0xffffffffu, wait_or_abort(&S.pass_full[pi % kPasses], (pi / kPasses) & 1u, abort)) != 0 &&
+           S.pass[pi % kPasses].more != 0;
+  };
+  auto done_pass = [&]() {   // (one arrival per warp)
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.pass_empty[pi % kPasses]);
+    ++pi;
+  };
+  auto all_wait = [&](uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort)) != 0;
+  };
+
+  if (warp < kLdWarps) {
+    // ================================================ window rows and Q
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsLoad));
+    const float qsign = a.scale < 0.f ? -1.f : 1.f;   // the logits' own factor is not negative
+    auto to_f16x2 = [&](uint32_t w) -> uint32_t {
+      const __half2 hv = __floats2half2_rn(bf16_to_f32(w & 0xFFFFu) * qsign, bf16_to_f32(w >> 16) * qsign);
+      return *reinterpret_cast<const uint32_t *>(&hv);
+    };
+    constexpr int LPK = D / 16, RPI = 32 / LPK;       // lanes per window row (16 bytes each), rows per warp access
+    const int kl = lane % LPK, kr = lane / LPK;
+    auto put_row = [&](int slot, uint4 v) {           // 16 channels of a key into the ring
+      uint32_t h[8];
+      e4m3x4_to_f16x2(no_nan(v.x), h);
+      e4m3x4_to_f16x2(no_nan(v.y), h + 2);
+      e4m3x4_to_f16x2(no_nan(v.z), h + 4);
+      e4m3x4_to_f16x2(no_nan(v.w), h + 6);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        *reinterpret_cast<uint4 *>(S.kr + sw_off(slot, 2 * kl + j, R)) = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
+    };
+    // Q chunk: 128 rows x 8 pieces of 16 bytes, four per thread
+    uint32_t qi = 0;
+    bool ok = true;
+    while (ok && next_pass()) {
+      const Pass &ps = S.pass[pi % kPasses];
+      const int row0 = ps.row0, nrows = ps.nrows;
+      const uint16_t *qrow = a.q + (size_t)row0 * D;
+      uint4 v[4];
+      auto load_q = [&](int c) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = tid + u * kLd, r = i >> 3, pc = i & 7;
+          v[u] = r < nrows ? __ldg(reinterpret_cast<const uint4 *>(qrow + (size_t)r * D + c * 64) + pc) : make_uint4(0, 0, 0, 0);
+        }
+      };
+      load_q(0);   // on its way while the window rows are brought
+      // ---- the rows that enter the ring
+      if (ps.wait_for > 0) {
+        int w_ok = 1;
+        if (lane == 0) {
+          const volatile int *done = &S.passes_done;
+          uint32_t i = 0;
+          while (*done < ps.wait_for) {
+            if (++i >= kWaitLimit || *abort) { w_ok = 0; *abort = 1; break; }
+            __nanosleep(64);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, w_ok, 0) != 0;
+        if (!ok) break;
+      }
+      const int b = ps.b;
+      if (ps.load_sinks) {
+        for (int s0 = warp * RPI; s0 < n_sink; s0 += kLdWarps * RPI) {
+          const int s = s0 + kr;
+          if (s < n_sink) put_row(s, __ldg(reinterpret_cast<const uint4 *>(a.sink_rows + ((size_t)b * a.sink_cap + s) * D) + kl));
+        }
+      }
+      {
+        constexpr int BATCH = 4;                      // accesses in flight
+        for (int t0 = ps.load_lo + warp * RPI; t0 < ps.end; t0 += kLdWarps * RPI * BATCH) {
+          uint4 w[BATCH];
+#pragma unroll
+          for (int u = 0; u < BATCH; ++u) {
+            const int t = t0 + u * kLdWarps * RPI + kr;
+            if (t < ps.end) w[u] = __ldg(reinterpret_cast<const uint4 *>(a.swa_rows + ((size_t)b * a.W_cap + t % a.W_cap) * D) + kl);
+          }
+#pragma unroll
+          for (int u = 0; u < BATCH; ++u) {
+            const int t = t0 + u * kLdWarps * RPI + kr;
+            if (t < ps.end) put_row(n_sink + t % rw, w[u]);
+          }
+        }
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.k_full[pi & 3u]);
+      // ---- Q
+#pragma unroll 1
+      for (int c = 0; c < NCH; ++c) {
+        uint4 o[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) o[u] = make_uint4(to_f16x2(v[u].x), to_f16x2(v[u].y), to_f16x2(v[u].z), to_f16x2(v[u].w));
+        if (c + 1 < NCH) load_q(c + 1);
+        const uint32_t slot = qi % kQSlots, ph = (qi / kQSlots) & 1u;
+        ++qi;
+        ok = all_wait(&S.q_empty[slot], ph ^ 1u);
+        if (!ok) break;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int i = tid + u * kLd, r = i >> 3, pc = i & 7;
+          *reinterpret_cast<uint4 *>(S.q[slot] + sw_off(r, pc, kRows)) = o[u];
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.q_full[slot]);
+      }
+      done_pass();
+    }
+  } else if (warp < kSmWarp0 + 4) {
+    // ================================================ softmax: thread = row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    const int q = warp & 3, row = 32 * q + lane;
+    const uint32_t lrow = tmem + ((uint32_t)(32 * q) << 16);
+    // logits in base 2; never a factor of 0, so that a hidden key's -inf stays
+    const float lw = fmaxf(fabsf(a.scale) * a.s_swa * kLog2e, 1e-30f);
+    const float ls = n_sink > 0 ? fmaxf(fabsf(a.scale) * a.s_sink * kLog2e, 1e-30f) : lw;
+    const float ow = a.window > 0 ? __log2f(a.s_swa) : 0.f, os = n_sink > 0 ? __log2f(a.s_sink) : 0.f;
+    const float rs_w = 1.f / exp2f(ow), rs_s = 1.f / exp2f(os);
+    bool ok = true;
+    while (ok && next_pass()) {
+      const Pass &ps = S.pass[pi % kPasses];
+      const int frow = ps.row0 + row;
+      const bool live = row < ps.nrows;
+      const int t = live ? ps.pos[frow / a.H - ps.q0] : -1;
+      // covered by this pass: its window lies in [lo, end) and no earlier pass covered it
+      const bool mine = live && (t < 0 ? ps.first != 0 : (t >= ps.from && t < ps.end));
+      // the slots this row sees, one bit per key
+      int wlo = a.window > 0 ? t - a.window + 1 : t + 1;
+      if (wlo < 0) wlo = 0;
+      constexpr int NW = (R + 31) / 32;
+      const int len = mine && t >= 0 && a.window > 0 ? t - wlo + 1 : 0;
+      const int s0 = n_sink + wlo % rw, e0 = s0 + len;              // [s0, e0), wrapping from R to n_sink
+      const int e1 = e0 < R ? e0 : R, w1 = e0 > R ? n_sink + e0 - R : n_sink;
+      const int ns = mine && t >= 0 ? (n_sink < wlo ? n_sink : wlo) : 0;
+      auto span = [&](int w, int lo, int hi) -> uint32_t {          // bits [lo, hi) of word w
+        lo -= 32 * w; hi -= 32 * w;
+        lo = lo < 0 ? 0 : lo; hi = hi > 32 ? 32 : hi;
+        return hi > lo ? (0xFFFFFFFFu >> (32 - (hi - lo))) << lo : 0u;
+      };
+      auto seen_word = [&](int w) -> uint32_t { return span(w, s0, e1) | span(w, n_sink, w1) | span(w, 0, ns); };
+      const uint32_t buf = pi & 1u, scol = lrow + kColS + buf * kSCols;
+      ok = all_wait(&S.s_full[buf], (pi >> 1) & 1u);
+      if (!ok) break;
+      tc_fence_after();
+      // (Words of 32 keys; what a last word of 16 reads behind the ring's keys
+      // has no bit set.)
+      // pass 1: the largest weight times scale, in base 2
+      float top = -INFINITY;
+#pragma unroll 1
+      for (int w = 0; w < NW; ++w) {
+        uint32_t rv[32];
+        tmem_ld_x32(scol + 32 * w, rv);
+        const uint32_t seen = seen_word(w), sinks = span(w, 0, n_sink);
+        tmem_wait_ld();
+        if (sinks == 0) {
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int j = 0; j < 32; ++j) m4[j & 3] = (seen >> j) & 1u ? fmaxf(m4[j & 3], __uint_as_float(rv[j])) : m4[j & 3];
+          top = fmaxf(top, fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), lw, ow));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const bool snk = (sinks >> j) & 1u;
+            const float y = fmaf(__uint_as_float(rv[j]), snk ? ls : lw, snk ? os : ow);
+            top = (seen >> j) & 1u ? fmaxf(top, y) : top;
+          }
+        }
+      }
+      const float mu = top == -INFINITY ? 0.f : top;
+      // pass 2: P, and the sums of the two sorts of keys
+      float sum_s = 0.f, sum_w = 0.f;
+#pragma unroll 1
+      for (int w = 0; w < NW; ++w) {
+        uint32_t rv[32], pr[16];
+        tmem_ld_x32(scol + 32 * w, rv);
+        const uint32_t seen = seen_word(w), sinks = span(w, 0, n_sink);
+        tmem_wait_ld();
+        float t2[2] = {0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+          float p[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const bool snk = (sinks >> (j + k)) & 1u;
+            const float y = fmaf(__uint_as_float(rv[j + k]), snk ? ls : lw, (snk ? os : ow) - mu);
+            p[k] = (seen >> (j + k)) & 1u ? ex2_approx(y) : 0.f;
+            t2[k] += snk ? 0.f : p[k];
+            sum_s += snk ? p[k] : 0.f;
+          }
+          const __half2 hv = __floats2half2_rn(p[0], p[1]);
+          pr[j / 2] = *reinterpret_cast<const uint32_t *>(&hv);
+        }
+        sum_w += t2[0] + t2[1];
+        tmem_st_x16(scol + 16 * w, pr);   // over columns whose S has been read
+      }
+      const float l = sum_s * rs_s + sum_w * rs_w;
+      S.linv[pi & 3u][row] = mine ? (l > 0.f ? 1.f / l : 0.f) : -1.f;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.p_full[buf]);
+      done_pass();
+    }
+  } else if (warp < kEpiWarp0) {
+    // ================================================ scheduler, MMA issuers (warp 13 has no work)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
+    if (warp == kSchedWarp) {
+      const int units = a.B * rt_own, rows = a.T_q * a.H;
+      const int u_end = (int)((long long)units * (blockIdx.x + 1) / gridDim.x);
+      int u = (int)((long long)units * blockIdx.x / gridDim.x);
+      int res_b = -1, res_lo = 0, res_hi = 0;          // ring: tokens [res_lo, res_hi) of sequence res_b
+      int old[kLive];                                  // first token of the last passes (newest first)
+#pragma unroll
+      for (int i = 0; i < kLive; ++i) old[i] = INT_MAX;
+      bool ok = true;
+      while (ok) {
+        const bool more = u < u_end;
+        const int b = u / rt_own, rt = u % rt_own;
+        const int row0 = b * rows + rt * kRows, nrows = rows - rt * kRows < kRows ? rows - rt * kRows : kRows;
+        int from = 0, first = 1;                       // passes of this tile
+        do {
+          Pass &ps = S.pass[pi % kPasses];
+          ok = all_wait(&S.pass_empty[pi % kPasses], ((pi / kPasses) & 1u) ^ 1u);
+          if (!ok) break;
+          if (!more) {
+            if (lane == 0) ps.more = 0;
+          } else {
+            const int q0 = row0 / a.H, nq = (row0 + nrows - 1) / a.H - q0 + 1;
+            int lo = INT_MAX;
+            for (int i = lane; i < nq; i += 32) {
+              int t = __ldg(a.q_pos + q0 + i);
+              if (t > kMaxPos) {
+                flag(a.status, CSA2_DEV_BAD_POSITION);
+                t = -1;
+              }
+              ps.pos[i] = t;
+              if (t >= from && t >= 0) {
+                int l = a.window > 0 ? t - a.window + 1 : t + 1;
+                l = l < 0 ? 0 : l;
+                lo = l < lo ? l : lo;
+              }
+            }
+            __syncwarp();
+            lo = __reduce_min_sync(0xffffffffu, lo);
+            // the queries whose windows lie in [lo, lo + rw) (no window: any)
+            int end = 0, next = INT_MAX;
+            if (lo != INT_MAX) {
+              const int lim = a.window > 0 ? lo + rw : INT_MAX;
+              for (int i = lane; i < nq; i += 32) {
+                const int t = ps.pos[i];
+                if (t >= from && t >= 0) {
+                  if (t < lim) end = t + 1 > end ? t + 1 : end;
+                  else next = t < next ? t : next;
+                }
+              }
+              end = __reduce_max_sync(0xffffffffu, end);
+              next = __reduce_min_sync(0xffffffffu, next);
+            } else {
+              lo = 0;
+            }
+            // rows that enter: behind what the ring holds, or all of them
+            const bool same = b == res_b && lo >= res_lo && lo <= res_hi;
+            int load_lo = same ? (res_hi < end ? res_hi : end) : lo;
+            if (a.window <= 0) load_lo = end;
+            int wait_for = 0;
+            if (b != res_b || !same) {
+              wait_for = (int)pi;
+            } else if (end > load_lo) {
+              // slots of tokens below end - rw are overwritten: every unfinished pass that needs one of them
+#pragma unroll
+              for (int i = kLive - 1; i >= 0; --i)
+                if (old[i] < end - rw) wait_for = (int)pi - i;
+            }
+            if (lane == 0) {
+              ps.more = 1; ps.row0 = row0; ps.nrows = nrows; ps.b = b; ps.q0 = q0; ps.nq = nq;
+              ps.lo = lo; ps.end = end; ps.from = from; ps.first = first;
+              ps.load_lo = load_lo; ps.load_sinks = b != res_b; ps.wait_for = wait_for;
+            }
+#pragma unroll
+            for (int i = kLive - 1; i > 0; --i) old[i] = old[i - 1];
+            old[0] = end > lo ? lo : INT_MAX;
+            if (!same) { res_lo = lo; res_hi = lo; }
+            res_b = b;
+            res_hi = end > res_hi ? end : res_hi;
+            if (res_lo < res_hi - rw) res_lo = res_hi - rw;
+            from = next == INT_MAX ? INT_MAX : end;
+            first = 0;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.pass_full[pi % kPasses]);
+          ++pi;
+        } while (more && from != INT_MAX);
+        ++u;
+        if (!more) break;
+      }
+    } else if (warp == kMmaWarp) {
+      // one lane runs the whole loop, its waits included (a converged warp that
+      // elects a lane per group of MMAs issues them at half the rate)
+      if (elect_one()) {
+        uint32_t qi = 0;
+        bool ok = true;
+        while (ok) {
+          ok = wait_or_abort(&S.pass_full[pi % kPasses], (pi / kPasses) & 1u, abort);
+          if (!ok || !S.pass[pi % kPasses].more) break;
+          mbar_arrive(&S.pass_empty[pi % kPasses]);
+          const uint32_t buf = pi & 1u, scol = tmem + kColS + buf * kSCols;
+          ok = wait_or_abort(&S.k_full[pi & 3u], (pi >> 2) & 1u, abort);
+          if (ok && pi >= 2) ok = wait_or_abort(&S.pv_done[buf], ((pi >> 1) & 1u) ^ 1u, abort);   // the buffer's last P has been used
+          if (!ok) break;
+#pragma unroll 1
+          for (int c = 0; c < NCH; ++c) {
+            const uint32_t slot = qi % kQSlots;
+            ok = wait_or_abort(&S.q_full[slot], (qi / kQSlots) & 1u, abort);
+            if (!ok) break;
+            ++qi;
+            tc_fence_after();
+            const uint64_t da = smem_desc_kmajor(smem_u32(S.q[slot]), 128);
+            const uint64_t db = smem_desc_kmajor(smem_u32(S.kr) + c * (R * 128), 128);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_f16(scol, da + ((kk * 32) >> 4), db + ((kk * 32) >> 4), kIdS, (c > 0 || kk > 0) ? 1u : 0u);
+            tc_commit(&S.q_empty[slot]);
+          }
+          if (!ok) break;
+          tc_commit(&S.s_full[buf]);
+          ++pi;
+        }
+      }
+      __syncwarp();
+    } else if (warp == kPvWarp) {
+      if (elect_one()) {
+        uint32_t oi = 0;
+        bool ok = true;
+        while (ok) {
+          ok = wait_or_abort(&S.pass_full[pi % kPasses], (pi / kPasses) & 1u, abort);
+          if (!ok || !S.pass[pi % kPasses].more) break;
+          mbar_arrive(&S.pass_empty[pi % kPasses]);
+          const uint32_t buf = pi & 1u, pcol = tmem + kColS + buf * kSCols;
+          ok = wait_or_abort(&S.p_full[buf], (pi >> 1) & 1u, abort);
+          if (!ok) break;
+#pragma unroll 1
+          for (int c = 0; c < NCH; ++c) {
+            const uint32_t ob = oi % kOBufs;
+            ok = wait_or_abort(&S.o_empty[ob], ((oi / kOBufs) & 1u) ^ 1u, abort);
+            if (!ok) break;
+            ++oi;
+            tc_fence_after();
+            const uint64_t dv = smem_desc_mnmajor_sw128(smem_u32(S.kr) + c * (R * 128), R * 128, 1024);
+#pragma unroll
+            for (int ks = 0; ks < R / 16; ++ks)
+              tc_mma_f16_ta(tmem + kColO + ob * 64, pcol + ks * 8, dv + ((2 * ks * 1024) >> 4), kIdO, ks > 0 ? 1u : 0u);
+            tc_commit(&S.o_full[ob]);
+          }
+          if (!ok) break;
+          tc_commit(&S.pv_done[buf]);
+          ++pi;
+        }
+      }
+      __syncwarp();
+    }
+  } else {
+    // ================================================ output
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
+    const int q = warp & 3;
+    const uint32_t lrow = tmem + ((uint32_t)(32 * q) << 16);
+    uint8_t *stage = S.stage[q];
+    uint32_t oi = 0;
+    bool ok = true;
+    while (ok && next_pass()) {
+      const int row0 = S.pass[pi % kPasses].row0 + 32 * q;
+      done_pass();   // (the descriptor is not needed any more; pi is the next pass's from here on)
+      float inv = -1.f;
+      uint32_t covered = 0;
+#pragma unroll 1
+      for (int c = 0; c < NCH; ++c) {
+        const uint32_t ob = oi % kOBufs;
+        ok = all_wait(&S.o_full[ob], (oi / kOBufs) & 1u);
+        if (!ok) break;
+        ++oi;
+        tc_fence_after();
+        if (c == 0) {   // the O product follows the softmax: its sums are there
+          inv = S.linv[(pi - 1) & 3u][32 * q + lane];
+          covered = __ballot_sync(0xffffffffu, inv >= 0.f);
+        }
+        uint32_t o[64];
+        tmem_ld_x32(lrow + kColO + ob * 64, o);
+        tmem_ld_x32(lrow + kColO + ob * 64 + 32, o + 32);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&S.o_empty[ob]);
+          if (c == NCH - 1 && q == 0) *reinterpret_cast<volatile int *>(&S.passes_done) = (int)pi;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {   // 32 channels: rows through the stage, whole sectors out
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int i = 32 * h + 8 * p + 2 * j;
+              const __nv_bfloat162 bv = __floats2bfloat162_rn(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
+              pk[j] = *reinterpret_cast<const uint32_t *>(&bv);
+            }
+            *reinterpret_cast<uint4 *>(stage + lane * 64 + ((p ^ ((lane >> 1) & 3)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + lane / 4, p = lane % 4;
+            const uint4 v = *reinterpret_cast<const uint4 *>(stage + r * 64 + ((p ^ ((r >> 1) & 3)) << 4));
+            if ((covered >> r) & 1u)
+              reinterpret_cast<uint4 *>(a.out + (size_t)(row0 + r) * D + c * 64 + h * 32)[p] = v;
+          }
+          __syncwarp();
+        }
+      }
+    }
+  }
+  // ---- every role is through, or a wait gave up
+  const bool dead = __syncthreads_or(*abort != 0) != 0;
+  if (dead) {
+    if (tid == 0) flag(a.status, CSA2_DEV_TIMEOUT);
+    if (warp == kMmaWarp || warp == kPvWarp) {   // every MMA issued so far is done before its memory goes
+      if (elect_one()) {
+        tc_commit(&S.fin);
+        mbar_wait_bounded(&S.fin, 0, kWaitLimit);
+      }
+      __syncwarp();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D>
+static cudaError_t launch_t(const DenseAttnArgs &a, int sms, cudaStream_t s) {
+  const size_t smem = sizeof(WinSmem<D>) + 1024;
+  static_assert(sizeof(WinSmem<D>) + 1024 <= 232448, "shared memory");
+  cudaError_t e = cudaFuncSetAttribute(attn_window_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const int rt_own = (a.T_q * a.H + kRows - 1) / kRows;
+  const long long units = (long long)a.B * rt_own;
+  const int grid = units < sms ? (int)units : sms;
+  return launch_pdl(attn_window_kernel<D>, dim3(grid), dim3(kThreads), smem, s, dim3(1, 1, 1), a, rt_own);
+}
+
+bool window_fits_ring(const DenseAttnArgs &a) {
+  const int nq = (kRows - 1 + a.H - 1) / a.H + 1;   // queries that 128 rows can touch
+  const int most = a.T_q < nq ? a.T_q : nq;
+  return a.n_sink + (a.window > 0 ? a.window + most - 1 : 0) <= ring_keys(a.D);
+}
+
+cudaError_t launch_window_ring(const DenseAttnArgs &a, int sms, cudaStream_t s) {
+  switch (a.D) {
+    case 128: return launch_t<128>(a, sms, s);
+    case 256: return launch_t<256>(a, sms, s);
+    default: return launch_t<512>(a, sms, s);
+  }
+}
+
+}  // namespace csa2

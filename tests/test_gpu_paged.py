@@ -527,6 +527,24 @@ def test_window_attention_padded_and_unordered_queries():
     run_window(1, 6, 64, 512, 128, 4, 0, seed=2, q_pos=[[300, -1, 299, 305, -1, 301]])
 
 
+@pytest.mark.parametrize("H,D", [(64, 512), (8, 128), (20, 256)])
+def test_window_attention_of_positions_far_apart(H, D):
+    # tiles whose queries' windows lie far from one another, before one another, and in several sequences
+    g = np.random.default_rng(H)
+    T, W = 37, 100
+    far = g.integers(0, 100000, T).tolist()
+    near = (500 + g.permutation(T)).tolist()
+    back = list(range(2000, 2000 - T, -1))
+    mixed = [far[i] if i % 5 == 0 else (-1 if i % 7 == 0 else 300 + i) for i in range(T)]
+    run_window(4, T, H, D, W, 4, 0, seed=3, q_pos=[far, near, back, mixed])
+
+
+def test_window_attention_keeps_its_ring_over_a_long_chunk():
+    # many more tokens than the ring of rows that a block keeps; unequal scales of sinks and window
+    run_window(1, 700, 16, 128, 40, 5, 10, seed=6, s_swa=2.0 ** -9, s_sink=64.0)
+    run_window(2, 300, 64, 256, 130, 12, 0, seed=7, s_swa=37.0, s_sink=0.01)
+
+
 def test_window_attention_without_a_window_sees_its_sinks():
     run_window(2, 3, 8, 256, 0, 9, 4, seed=3)
 
