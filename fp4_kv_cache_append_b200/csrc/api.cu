@@ -775,7 +775,14 @@ csa2_status csa2_window_attn(const csa2_swa_cache *swa, const csa2_swa_cache *si
   }
   a.q = q; a.q_pos = q_pos; a.B = swa->B; a.T_q = T_q; a.H = H; a.D = swa->D;
   a.scale = softmax_scale; a.out = out; a.ws = ws; a.status = d->status;
-  cudaError_t e = launch_window_attn(a, d->sms, reinterpret_cast<cudaStream_t>(stream));
+  cudaError_t e;
+  if (window_fits_ring(a)) {
+    CUtensorMap q_map;
+    if ((st = encode_bf16_map(q, (int64_t)a.B * T_q * H, a.D, 128, &q_map)) != CSA2_OK) return st;
+    e = launch_window_ring(q_map, a, d->sms, reinterpret_cast<cudaStream_t>(stream));
+  } else {
+    e = launch_window_attn(a, d->sms, reinterpret_cast<cudaStream_t>(stream));
+  }
   return e == cudaSuccess ? CSA2_OK : cuda_fail(e, "window attention launch");
 }
 

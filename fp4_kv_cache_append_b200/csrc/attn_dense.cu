@@ -1216,7 +1216,6 @@ cudaError_t launch_prefix_attn(const DenseAttnArgs &a, int sms, cudaStream_t s) 
 }
 size_t window_attn_workspace_bytes(int, int, int, int, int, int, int) { return 0; }
 cudaError_t launch_window_attn(const DenseAttnArgs &a, int sms, cudaStream_t s) {
-  if (window_fits_ring(a)) return launch_window_ring(a, sms, s);
   switch (a.D) {
     case 128: return launch_window_t<128>(a, sms, s);
     case 256: return launch_window_t<256>(a, sms, s);

@@ -6,30 +6,36 @@
 //   first tokens before it, K = V shared by the heads.
 //
 // A block walks over consecutive row tiles of a sequence and keeps the window's
-// rows as an fp16 ring in shared memory (slot = token mod ring size; the order
-// of keys does not matter, a row's visible slots are a bit mask), so each window
-// row is fetched and converted once per block, not once per query.  All keys of
-// a tile are in one S = Q K^T (M 128, N = ring), so the softmax needs no running
-// maximum and O no rescaling: O = P V is formed 64 channels at a time in a
-// three-deep ring of tensor-memory columns and stored as it is formed.  What is
-// left is the traffic of q and the output, 4 bytes per (row, channel), which
-// bounds the kernel (132 FLOP per byte at a window of 128 and D 512).
+// rows as a bf16 ring in shared memory (E4M3 is exact in bf16; slot = token mod
+// ring size: the order of keys does not matter, a row's visible slots are a bit
+// mask), so each window row is fetched and converted once per block, not once
+// per query, and Q goes from memory to the tensor core by TMA as it is.  All
+// keys of a tile are in one S = Q K^T (M 128, N = ring), so the softmax needs no
+// running maximum and O no rescaling.  P is split into two bf16 terms (their sum
+// is within 2^-17 of P): O = P V takes twice the products, which the tensor
+// cores have to spare, instead of a conversion of Q, which the other warps have
+// not.  O is formed 64 channels at a time in a three-deep ring of
+// tensor-memory columns and stored as it is formed.  What is left is the traffic
+// of q and the output, 4 bytes per (row, channel), which bounds the kernel (132
+// FLOP per byte at a window of 128 and D 512).
 // Warp roles, all persistent, handing work over through mbarriers:
-//   warps 0-7    new window rows (E4M3 -> fp16), then Q (bf16 -> fp16) chunk by
-//                chunk (64 channels) into a ring of A operands, the next chunk's
-//                loads in flight
-//   warps 8-11   softmax, one row per thread; P replaces S in tensor memory
-//   warp 12, 14  tcgen05.mma issuers of S and of O (one lane each)
-//   warp 15      scheduler: passes (below) through a ring of three descriptors
-//   warps 16-19  O / l -> bf16 -> output, through a per-warp staging tile so that
-//                whole sectors are stored
+//   warps 0-3    softmax, one row per thread, a row's logits in registers; P
+//                replaces S in tensor memory
+//   warps 4-7    O / l -> bf16 -> output, through a per-warp staging tile so that
+//                whole lines are stored
+//   warps 8, 10  tcgen05.mma issuers of S and of O (one lane each)
+//   warp 9       TMA loads of Q, 64 channels at a time
+//   warp 11      scheduler: passes (below) through a ring of three descriptors
+//   warps 12-15  new window rows into the ring (the first pass's, all of a
+//                window, by the softmax and output warps too)
 // A pass is a row tile with the range of tokens it needs; a tile whose queries'
 // windows do not fit one range (positions far apart) takes several passes, each
 // storing the rows it covers.  Sinks and window rows enter unscaled; with y =
 // log2 of a weight times its key's scale, P = 2^(y - max y) and the sum of the
 // weights is sum(P of sinks) / s_sink + sum(P of window) / s_window.
 // Every wait is bounded: one that gives up flags the device status and stops
-// every role; issued MMAs are drained and TMEM freed before the block exits.
+// every role; issued MMAs and copies are drained and TMEM freed before the block
+// exits.
 #include "attn_dense.cuh"
 #include "kernels.h"
 
@@ -37,21 +43,20 @@ namespace csa2 {
 
 namespace {
 
-constexpr int kLdWarps = 8;                  // window rows and Q
-constexpr int kSmWarp0 = 8, kMmaWarp = 12, kPvWarp = 14, kSchedWarp = 15, kEpiWarp0 = 16;
-constexpr int kThreads = 20 * 32;
-constexpr int kLd = kLdWarps * 32;
-// Registers per thread of the five warpgroups (2 x load, softmax, MMA, output);
-// their sum is at most the launch's 5 x 96.
-constexpr int kRegsLoad = 96, kRegsSoftmax = 112, kRegsMma = 72, kRegsEpi = 104;
+constexpr int kEpiWarp0 = 4, kMmaWarp = 8, kQWarp = 9, kPvWarp = 10, kSchedWarp = 11, kKeyWarp0 = 12, kKeyWarps = 4;
+constexpr int kThreads = 16 * 32;
+constexpr int kFirstWarps = 12;              // warps that bring the first pass's window rows
+// Registers per thread of the warpgroups (softmax, output, MMA, keys); their
+// sum is at most the launch's 4 x 128.
+constexpr int kRegsSoftmax = 232, kRegsEpi = 112, kRegsMma = 72, kRegsKeys = 96;
 constexpr int kPasses = 3;                   // descriptors
-constexpr int kQSlots = 4;                   // ring of Q chunks (so the loaders are at most three passes ahead of S)
 constexpr int kOBufs = 3;                    // ring of 64-channel O blocks
 constexpr int kLive = 8;                     // passes that can be unfinished at once (bounded by the rings above)
 constexpr uint32_t kTmemCols = 512;
 
-// Keys that the ring holds (N of S): 144 KB at D 512.
+// Keys that the ring holds (N of S): 144 KB at D 512; 64-channel chunks of Q in flight.
 __host__ __device__ constexpr int ring_keys(int D) { return D == 512 ? 144 : 160; }
+__host__ __device__ constexpr int q_slots(int D) { return D == 512 ? 3 : 4; }
 
 struct Pass {
   int more;                // 0: no further pass
@@ -68,12 +73,12 @@ struct Pass {
 
 template <int D>
 struct WinSmem {
-  static constexpr int R = ring_keys(D);
+  static constexpr int R = ring_keys(D), QSL = q_slots(D);
   alignas(1024) uint8_t kr[(D / 64) * R * 128];     // ring: chunks of [R keys x 128 B]
-  alignas(1024) uint8_t q[kQSlots][kRows * 128];    // Q chunks
-  alignas(16) uint8_t stage[4][32 * 64];            // per output warp: 32 rows x 32 channels bf16
+  alignas(1024) uint8_t q[QSL][kRows * 128];        // Q chunks
+  alignas(16) uint8_t stage[4][32 * 128];           // per output warp: 32 rows x 64 channels bf16
   float linv[4][kRows];                             // 1 / l of a pass's rows, negative: not covered
-  uint64_t q_full[kQSlots], q_empty[kQSlots], k_full[4], s_full[2], p_full[2], pv_done[2];
+  uint64_t q_full[QSL], q_empty[QSL], k_full[4], k_first, s_full[2], p_full[2], pv_done[2];
   uint64_t o_full[kOBufs], o_empty[kOBufs], pass_full[kPasses], pass_empty[kPasses], fin;
   uint32_t tmem_base;
   int abort;
@@ -85,13 +90,6 @@ struct WinSmem {
 constexpr uint32_t kSCols = 160, kColS = 0, kColO = 2 * kSCols;
 static_assert(kColO + kOBufs * 64 <= kTmemCols, "tensor memory");
 
-__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t *r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
 
 // E4M3 bytes with the NaN codes (0x7F, 0xFF) made zero: rows between two
 // queries' windows may never have been written.
@@ -103,10 +101,11 @@ __device__ __forceinline__ uint32_t no_nan(uint32_t w) {
 }  // namespace
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAttnArgs a, const int rt_own) {
-  constexpr int R = ring_keys(D), NCH = D / 64;
-  constexpr uint32_t kIdS = mma_idesc(kRows, R, 0u, 0u);
-  constexpr uint32_t kIdO = mma_idesc(kRows, 64, 0u, 0u) | (1u << 16);   // B (V) MN-major
+__global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAttnArgs a, const int rt_own,
+                                                                  const __grid_constant__ CUtensorMap q_map) {
+  constexpr int R = ring_keys(D), QSL = q_slots(D), NCH = D / 64;
+  constexpr uint32_t kIdS = mma_idesc(kRows, R, 1u, 1u);
+  constexpr uint32_t kIdO = mma_idesc(kRows, 64, 1u, 1u) | (1u << 16);   // B (V) MN-major
   extern __shared__ uint8_t smem_raw[];
   WinSmem<D> &S = *reinterpret_cast<WinSmem<D> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   volatile int *abort = &S.abort;
@@ -114,15 +113,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
   const int n_sink = a.n_sink, rw = R - n_sink > 0 ? R - n_sink : 1;   // ring: slots [0, n_sink) sinks, then token mod rw
   pdl_launch_dependents();
   if (tid == 0) {
-    for (int i = 0; i < kQSlots; ++i) { mbar_init(&S.q_full[i], kLdWarps); mbar_init(&S.q_empty[i], 1); }
-    for (int i = 0; i < 4; ++i) mbar_init(&S.k_full[i], kLdWarps);
+    for (int i = 0; i < QSL; ++i) { mbar_init(&S.q_full[i], 1); mbar_init(&S.q_empty[i], 1); }
+    for (int i = 0; i < 4; ++i) mbar_init(&S.k_full[i], kKeyWarps);
+    mbar_init(&S.k_first, kFirstWarps);
     for (int i = 0; i < 2; ++i) { mbar_init(&S.s_full[i], 1); mbar_init(&S.p_full[i], 4); mbar_init(&S.pv_done[i], 1); }
     for (int i = 0; i < kOBufs; ++i) { mbar_init(&S.o_full[i], 1); mbar_init(&S.o_empty[i], 4); }
-    for (int i = 0; i < kPasses; ++i) { mbar_init(&S.pass_full[i], 1); mbar_init(&S.pass_empty[i], kLdWarps + 4 + 4 + 2); }
+    // readers of a descriptor: key, softmax and output warps, S, O, Q
+    for (int i = 0; i < kPasses; ++i) { mbar_init(&S.pass_full[i], 1); mbar_init(&S.pass_empty[i], kKeyWarps + 4 + 4 + 3); }
     mbar_init(&S.fin, 2);
     S.abort = 0;
     S.passes_done = 0;
     fence_barrier_init();
+    prefetch_tmap(&q_map);
   }
   // slots that no row has entered hold zeros
   for (int i = tid; i < NCH * R * 8; i += kThreads) reinterpret_cast<uint4 *>(S.kr)[i] = make_uint4(0, 0, 0, 0);
@@ -143,25 +145,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
     return __all_sync(0xffffffffu, wait_or_abort(&S.pass_full[pi % kPasses], (pi / kPasses) & 1u, abort)) != 0 &&
            S.pass[pi % kPasses].more != 0;
   };
-  auto done_pass = [&]() {   // (one arrival per warp)
+  auto free_pass = [&]() {   // the descriptor is not needed any more (one arrival per warp)
     __syncwarp();
     if (lane == 0) mbar_arrive(&S.pass_empty[pi % kPasses]);
-    ++pi;
   };
-  auto all_wait = [&](uint64_t *bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort)) != 0;
-  };
-
-  if (warp < kLdWarps) {
-    // ================================================ window rows and Q
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsLoad));
-    const float qsign = a.scale < 0.f ? -1.f : 1.f;   // the logits' own factor is not negative
-    auto to_f16x2 = [&](uint32_t w) -> uint32_t {
-      const __half2 hv = __floats2half2_rn(bf16_to_f32(w & 0xFFFFu) * qsign, bf16_to_f32(w >> 16) * qsign);
-      return *reinterpret_cast<const uint32_t *>(&hv);
-    };
+  // The rows that enter the ring for a pass: this warp's share (w of nw).
+  auto bring_rows = [&](const Pass &ps, int w, int nw, uint64_t *bar) {
     constexpr int LPK = D / 16, RPI = 32 / LPK;       // lanes per window row (16 bytes each), rows per warp access
-    const int kl = lane % LPK, kr = lane / LPK;
+    constexpr int BATCH = 8;                          // accesses in flight
+    const int kl = lane % LPK, kr = lane / LPK, b = ps.b;
     auto put_row = [&](int slot, uint4 v) {           // 16 channels of a key into the ring
       uint32_t h[8];
       e4m3x4_to_f16x2(no_nan(v.x), h);
@@ -169,100 +161,68 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
       e4m3x4_to_f16x2(no_nan(v.z), h + 4);
       e4m3x4_to_f16x2(no_nan(v.w), h + 6);
 #pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[j]));
+        const __nv_bfloat162 v2 = __floats2bfloat162_rn(f.x, f.y);
+        h[j] = *reinterpret_cast<const uint32_t *>(&v2);
+      }
+#pragma unroll
       for (int j = 0; j < 2; ++j)
         *reinterpret_cast<uint4 *>(S.kr + sw_off(slot, 2 * kl + j, R)) = make_uint4(h[4 * j], h[4 * j + 1], h[4 * j + 2], h[4 * j + 3]);
     };
-    // Q chunk: 128 rows x 8 pieces of 16 bytes, four per thread
-    uint32_t qi = 0;
-    bool ok = true;
-    while (ok && next_pass()) {
-      const Pass &ps = S.pass[pi % kPasses];
-      const int row0 = ps.row0, nrows = ps.nrows;
-      const uint16_t *qrow = a.q + (size_t)row0 * D;
-      uint4 v[4];
-      auto load_q = [&](int c) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int i = tid + u * kLd, r = i >> 3, pc = i & 7;
-          v[u] = r < nrows ? __ldg(reinterpret_cast<const uint4 *>(qrow + (size_t)r * D + c * 64) + pc) : make_uint4(0, 0, 0, 0);
-        }
-      };
-      load_q(0);   // on its way while the window rows are brought
-      // ---- the rows that enter the ring
-      if (ps.wait_for > 0) {
-        int w_ok = 1;
-        if (lane == 0) {
-          const volatile int *done = &S.passes_done;
-          uint32_t i = 0;
-          while (*done < ps.wait_for) {
-            if (++i >= kWaitLimit || *abort) { w_ok = 0; *abort = 1; break; }
-            __nanosleep(64);
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, w_ok, 0) != 0;
-        if (!ok) break;
-      }
-      const int b = ps.b;
-      if (ps.load_sinks) {
-        for (int s0 = warp * RPI; s0 < n_sink; s0 += kLdWarps * RPI) {
-          const int s = s0 + kr;
-          if (s < n_sink) put_row(s, __ldg(reinterpret_cast<const uint4 *>(a.sink_rows + ((size_t)b * a.sink_cap + s) * D) + kl));
-        }
-      }
-      {
-        constexpr int BATCH = 4;                      // accesses in flight
-        for (int t0 = ps.load_lo + warp * RPI; t0 < ps.end; t0 += kLdWarps * RPI * BATCH) {
-          uint4 w[BATCH];
-#pragma unroll
-          for (int u = 0; u < BATCH; ++u) {
-            const int t = t0 + u * kLdWarps * RPI + kr;
-            if (t < ps.end) w[u] = __ldg(reinterpret_cast<const uint4 *>(a.swa_rows + ((size_t)b * a.W_cap + t % a.W_cap) * D) + kl);
-          }
-#pragma unroll
-          for (int u = 0; u < BATCH; ++u) {
-            const int t = t0 + u * kLdWarps * RPI + kr;
-            if (t < ps.end) put_row(n_sink + t % rw, w[u]);
-          }
-        }
-      }
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&S.k_full[pi & 3u]);
-      // ---- Q
+    if (ps.load_sinks) {
 #pragma unroll 1
-      for (int c = 0; c < NCH; ++c) {
-        uint4 o[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) o[u] = make_uint4(to_f16x2(v[u].x), to_f16x2(v[u].y), to_f16x2(v[u].z), to_f16x2(v[u].w));
-        if (c + 1 < NCH) load_q(c + 1);
-        const uint32_t slot = qi % kQSlots, ph = (qi / kQSlots) & 1u;
-        ++qi;
-        ok = all_wait(&S.q_empty[slot], ph ^ 1u);
-        if (!ok) break;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int i = tid + u * kLd, r = i >> 3, pc = i & 7;
-          *reinterpret_cast<uint4 *>(S.q[slot] + sw_off(r, pc, kRows)) = o[u];
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.q_full[slot]);
-      }
-      done_pass();
+      for (int s = w * RPI + kr; s < n_sink; s += nw * RPI)
+        put_row(s, __ldg(reinterpret_cast<const uint4 *>(a.sink_rows + ((size_t)b * a.sink_cap + s) * D) + kl));
     }
-  } else if (warp < kSmWarp0 + 4) {
+    // token t: row t mod W_cap of the sequence, slot t mod rw of the ring, both advanced without dividing again
+    int t = ps.load_lo + w * RPI + kr;
+    const int step = nw * RPI;
+    if (t < ps.end) {
+      int src = t % a.W_cap, slot = t % rw;
+      const int src_step = step % a.W_cap, slot_step = step % rw;
+      const uint4 *base = reinterpret_cast<const uint4 *>(a.swa_rows + (size_t)b * a.W_cap * D) + kl;
+#pragma unroll 1
+      while (t < ps.end) {
+        uint4 v[BATCH];
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+          v[u] = t + u * step < ps.end ? __ldg(base + (size_t)src * (D / 16)) : make_uint4(0, 0, 0, 0);
+          src += src_step;
+          if (src >= a.W_cap) src -= a.W_cap;
+        }
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+          if (t < ps.end) put_row(n_sink + slot, v[u]);
+          t += step;
+          slot += slot_step;
+          if (slot >= rw) slot -= rw;
+        }
+      }
+    }
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
+  auto all_wait = [&](uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort)) != 0;
+  };
+
+  if (warp < kEpiWarp0) {
     // ================================================ softmax: thread = row
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int q = warp & 3, row = 32 * q + lane;
     const uint32_t lrow = tmem + ((uint32_t)(32 * q) << 16);
-    // logits in base 2; never a factor of 0, so that a hidden key's -inf stays
-    const float lw = fmaxf(fabsf(a.scale) * a.s_swa * kLog2e, 1e-30f);
-    const float ls = n_sink > 0 ? fmaxf(fabsf(a.scale) * a.s_sink * kLog2e, 1e-30f) : lw;
-    const float ow = a.window > 0 ? __log2f(a.s_swa) : 0.f, os = n_sink > 0 ? __log2f(a.s_sink) : 0.f;
-    const float rs_w = 1.f / exp2f(ow), rs_s = 1.f / exp2f(os);
+    // y = log2(weight x key scale) = S x l + o, with the sign of the softmax
+    // scale taken into S and the factor never 0, so that a hidden key's -inf stays
+    const float s_win = a.window > 0 ? a.s_swa : a.s_sink, s_snk = n_sink > 0 ? a.s_sink : s_win;
+    const float lw = fmaxf(fabsf(a.scale) * s_win * kLog2e, 1e-30f), ls = fabsf(a.scale) * s_snk * kLog2e;
+    const float rs_w = 1.f / s_win, rs_s = 1.f / s_snk;
+    const float s2w = ls / lw, o2w = (log2f(s_snk) - log2f(s_win)) / lw;   // a sink's S as a window row's of the same y
     bool ok = true;
     while (ok && next_pass()) {
       const Pass &ps = S.pass[pi % kPasses];
+      if (pi == 0) bring_rows(ps, warp, kFirstWarps, &S.k_first);
       const int frow = ps.row0 + row;
       const bool live = row < ps.nrows;
       const int t = live ? ps.pos[frow / a.H - ps.q0] : -1;
@@ -286,67 +246,137 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
       ok = all_wait(&S.s_full[buf], (pi >> 1) & 1u);
       if (!ok) break;
       tc_fence_after();
-      // (Words of 32 keys; what a last word of 16 reads behind the ring's keys
-      // has no bit set.)
-      // pass 1: the largest weight times scale, in base 2
+      uint32_t sv[NW * 32];   // (what a last word of 16 reads behind the ring's keys has no bit set)
+#pragma unroll
+      for (int w = 0; w < NW; ++w) tmem_ld_x32(scol + 32 * w, sv + 32 * w);
+      tmem_wait_ld();
       float top = -INFINITY;
-#pragma unroll 1
+#pragma unroll
       for (int w = 0; w < NW; ++w) {
-        uint32_t rv[32];
-        tmem_ld_x32(scol + 32 * w, rv);
-        const uint32_t seen = seen_word(w), sinks = span(w, 0, n_sink);
-        tmem_wait_ld();
-        if (sinks == 0) {
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        const uint32_t seen = seen_word(w);
+        uint32_t *x = sv + 32 * w;
+        if (a.scale < 0.f) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) m4[j & 3] = (seen >> j) & 1u ? fmaxf(m4[j & 3], __uint_as_float(rv[j])) : m4[j & 3];
-          top = fmaxf(top, fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), lw, ow));
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const bool snk = (sinks >> j) & 1u;
-            const float y = fmaf(__uint_as_float(rv[j]), snk ? ls : lw, snk ? os : ow);
-            top = (seen >> j) & 1u ? fmaxf(top, y) : top;
-          }
+          for (int j = 0; j < 32; ++j) x[j] ^= 0x80000000u;
         }
+        if (32 * w < n_sink) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (32 * w + j < n_sink) x[j] = __float_as_uint(fmaf(__uint_as_float(x[j]), s2w, o2w));
+        }
+        if (!__all_sync(0xffffffffu, seen == 0xFFFFFFFFu)) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (!((seen >> j) & 1u)) x[j] = 0xFF800000u;
+        }
+        float m4[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m4[j] = __uint_as_float(x[j]);
+#pragma unroll
+        for (int j = 4; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], __uint_as_float(x[j]));
+        top = fmaxf(top, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
       }
-      const float mu = top == -INFINITY ? 0.f : top;
-      // pass 2: P, and the sums of the two sorts of keys
-      float sum_s = 0.f, sum_w = 0.f;
-#pragma unroll 1
+      // P = 2^(y - max y) = hi + lo, in place (columns [0, 16) and [16, 32) of
+      // the word's 32), and the sums of the two sorts of keys
+      const float mu = top == -INFINITY ? 0.f : top * lw;
+      float sum_s = 0.f;
+      uint64_t sum2 = 0;
+      const uint64_t l2 = f32x2(lw, lw), m2 = f32x2(-mu, -mu);
+#pragma unroll
       for (int w = 0; w < NW; ++w) {
-        uint32_t rv[32], pr[16];
-        tmem_ld_x32(scol + 32 * w, rv);
-        const uint32_t seen = seen_word(w), sinks = span(w, 0, n_sink);
-        tmem_wait_ld();
-        float t2[2] = {0.f, 0.f};
+        uint32_t pr[32];
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
-          float p[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const bool snk = (sinks >> (j + k)) & 1u;
-            const float y = fmaf(__uint_as_float(rv[j + k]), snk ? ls : lw, (snk ? os : ow) - mu);
-            p[k] = (seen >> (j + k)) & 1u ? ex2_approx(y) : 0.f;
-            t2[k] += snk ? 0.f : p[k];
-            sum_s += snk ? p[k] : 0.f;
+          const uint32_t *x = sv + 32 * w + j;
+          const float2 y = unpack_f32x2(fma_f32x2(f32x2(__uint_as_float(x[0]), __uint_as_float(x[1])), l2, m2));
+          const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
+          float w0 = p0, w1 = p1;
+          if (32 * w < n_sink) {   // (a word with sinks)
+            const bool k0 = 32 * w + j < n_sink, k1 = 32 * w + j + 1 < n_sink;
+            sum_s += (k0 ? p0 : 0.f) + (k1 ? p1 : 0.f);
+            w0 = k0 ? 0.f : p0;
+            w1 = k1 ? 0.f : p1;
           }
-          const __half2 hv = __floats2half2_rn(p[0], p[1]);
-          pr[j / 2] = *reinterpret_cast<const uint32_t *>(&hv);
+          sum2 = add_f32x2(sum2, f32x2(w0, w1));
+          const __nv_bfloat162 hv = __floats2bfloat162_rn(p0, p1);
+          const uint32_t hi = *reinterpret_cast<const uint32_t *>(&hv);
+          const __nv_bfloat162 lv = __floats2bfloat162_rn(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xFFFF0000u));
+          pr[j / 2] = hi;
+          pr[16 + j / 2] = *reinterpret_cast<const uint32_t *>(&lv);
         }
-        sum_w += t2[0] + t2[1];
-        tmem_st_x16(scol + 16 * w, pr);   // over columns whose S has been read
+        tmem_st_x32(scol + 32 * w, pr);
       }
+      const float2 st2 = unpack_f32x2(sum2);
+      const float sum_w = st2.x + st2.y;
       const float l = sum_s * rs_s + sum_w * rs_w;
       S.linv[pi & 3u][row] = mine ? (l > 0.f ? 1.f / l : 0.f) : -1.f;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.p_full[buf]);
-      done_pass();
+      free_pass();
+      ++pi;
     }
-  } else if (warp < kEpiWarp0) {
-    // ================================================ scheduler, MMA issuers (warp 13 has no work)
+  } else if (warp < kMmaWarp) {
+    // ================================================ output
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
+    const int q = warp & 3;
+    const uint32_t lrow = tmem + ((uint32_t)(32 * q) << 16);
+    uint8_t *stage = S.stage[q];
+    uint32_t oi = 0;
+    bool ok = true;
+    while (ok && next_pass()) {
+      const int row0 = S.pass[pi % kPasses].row0 + 32 * q;
+      if (pi == 0) bring_rows(S.pass[0], 4 + q, kFirstWarps, &S.k_first);
+      free_pass();
+      ++pi;   // (passes done when this one is)
+      float inv = -1.f;
+      uint32_t covered = 0;
+#pragma unroll 1
+      for (int c = 0; c < NCH; ++c) {
+        const uint32_t ob = oi % kOBufs;
+        ok = all_wait(&S.o_full[ob], (oi / kOBufs) & 1u);
+        if (!ok) break;
+        ++oi;
+        tc_fence_after();
+        if (c == 0) {   // the O product follows the softmax: its sums are there
+          inv = S.linv[(pi - 1) & 3u][32 * q + lane];
+          covered = __ballot_sync(0xffffffffu, inv >= 0.f);
+        }
+        uint32_t o[64];
+        tmem_ld_x32(lrow + kColO + ob * 64, o);
+        tmem_ld_x32(lrow + kColO + ob * 64 + 32, o + 32);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&S.o_empty[ob]);
+          if (c == NCH - 1 && q == 0) *reinterpret_cast<volatile int *>(&S.passes_done) = (int)pi;
+        }
+        // rows through the stage, whole lines out
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          uint32_t pk[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int i = 8 * p + 2 * j;
+            const __nv_bfloat162 bv = __floats2bfloat162_rn(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
+            pk[j] = *reinterpret_cast<const uint32_t *>(&bv);
+          }
+          *reinterpret_cast<uint4 *>(stage + lane * 128 + ((p ^ (lane & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = 4 * i + lane / 8, p = lane % 8;
+          const uint4 v = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((p ^ (r & 7)) << 4));
+          if ((covered >> r) & 1u) reinterpret_cast<uint4 *>(a.out + (size_t)(row0 + r) * D + c * 64)[p] = v;
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp < kKeyWarp0) {
+    // ================================================ scheduler, MMA issuers, Q
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
     if (warp == kSchedWarp) {
       const int units = a.B * rt_own, rows = a.T_q * a.H;
@@ -434,8 +464,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
           if (lane == 0) mbar_arrive(&S.pass_full[pi % kPasses]);
           ++pi;
         } while (more && from != INT_MAX);
-        ++u;
         if (!more) break;
+        ++u;
       }
     } else if (warp == kMmaWarp) {
       // one lane runs the whole loop, its waits included (a converged warp that
@@ -448,13 +478,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
           if (!ok || !S.pass[pi % kPasses].more) break;
           mbar_arrive(&S.pass_empty[pi % kPasses]);
           const uint32_t buf = pi & 1u, scol = tmem + kColS + buf * kSCols;
-          ok = wait_or_abort(&S.k_full[pi & 3u], (pi >> 2) & 1u, abort);
+          ok = pi == 0 ? wait_or_abort(&S.k_first, 0, abort) : wait_or_abort(&S.k_full[pi & 3u], (pi >> 2) & 1u, abort);
           if (ok && pi >= 2) ok = wait_or_abort(&S.pv_done[buf], ((pi >> 1) & 1u) ^ 1u, abort);   // the buffer's last P has been used
           if (!ok) break;
 #pragma unroll 1
           for (int c = 0; c < NCH; ++c) {
-            const uint32_t slot = qi % kQSlots;
-            ok = wait_or_abort(&S.q_full[slot], (qi / kQSlots) & 1u, abort);
+            const uint32_t slot = qi % QSL;
+            ok = wait_or_abort(&S.q_full[slot], (qi / QSL) & 1u, abort);
             if (!ok) break;
             ++qi;
             tc_fence_after();
@@ -469,6 +499,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
           tc_commit(&S.s_full[buf]);
           ++pi;
         }
+      }
+      __syncwarp();
+    } else if (warp == kQWarp) {
+      if (elect_one()) {
+        uint32_t qi = 0;
+        bool ok = true;
+        while (ok) {
+          ok = wait_or_abort(&S.pass_full[pi % kPasses], (pi / kPasses) & 1u, abort);
+          if (!ok || !S.pass[pi % kPasses].more) break;
+          const int row0 = S.pass[pi % kPasses].row0;
+          mbar_arrive(&S.pass_empty[pi % kPasses]);
+#pragma unroll 1
+          for (int c = 0; c < NCH; ++c) {   // (rows behind the tile's last one are some other rows or zeros: never used)
+            const uint32_t slot = qi % QSL;
+            ok = wait_or_abort(&S.q_empty[slot], ((qi / QSL) & 1u) ^ 1u, abort);
+            if (!ok) break;
+            ++qi;
+            mbar_arrive_expect_tx(&S.q_full[slot], kRows * 128);
+            tma_load_2d(S.q[slot], &q_map, c * 64, row0, &S.q_full[slot]);
+          }
+          ++pi;
+        }
+        if (!ok)   // copies in flight land before the block may end
+          for (uint32_t i = 1; i <= (uint32_t)QSL && i <= qi; ++i)
+            mbar_wait_bounded(&S.q_full[(qi - i) % QSL], ((qi - i) / QSL) & 1u, kWaitLimit);
       }
       __syncwarp();
     } else if (warp == kPvWarp) {
@@ -492,7 +547,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
             const uint64_t dv = smem_desc_mnmajor_sw128(smem_u32(S.kr) + c * (R * 128), R * 128, 1024);
 #pragma unroll
             for (int ks = 0; ks < R / 16; ++ks)
-              tc_mma_f16_ta(tmem + kColO + ob * 64, pcol + ks * 8, dv + ((2 * ks * 1024) >> 4), kIdO, ks > 0 ? 1u : 0u);
+#pragma unroll
+              for (int lo = 0; lo < 2; ++lo)
+                tc_mma_f16_ta(tmem + kColO + ob * 64, pcol + 32 * (ks / 2) + 8 * (ks % 2) + 16 * lo,
+                              dv + ((2 * ks * 1024) >> 4), kIdO, (ks > 0 || lo > 0) ? 1u : 0u);
             tc_commit(&S.o_full[ob]);
           }
           if (!ok) break;
@@ -503,63 +561,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
       __syncwarp();
     }
   } else {
-    // ================================================ output
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
-    const int q = warp & 3;
-    const uint32_t lrow = tmem + ((uint32_t)(32 * q) << 16);
-    uint8_t *stage = S.stage[q];
-    uint32_t oi = 0;
+    // ================================================ window rows
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsKeys));
+    const int kw = warp - kKeyWarp0;
     bool ok = true;
     while (ok && next_pass()) {
-      const int row0 = S.pass[pi % kPasses].row0 + 32 * q;
-      done_pass();   // (the descriptor is not needed any more; pi is the next pass's from here on)
-      float inv = -1.f;
-      uint32_t covered = 0;
-#pragma unroll 1
-      for (int c = 0; c < NCH; ++c) {
-        const uint32_t ob = oi % kOBufs;
-        ok = all_wait(&S.o_full[ob], (oi / kOBufs) & 1u);
-        if (!ok) break;
-        ++oi;
-        tc_fence_after();
-        if (c == 0) {   // the O product follows the softmax: its sums are there
-          inv = S.linv[(pi - 1) & 3u][32 * q + lane];
-          covered = __ballot_sync(0xffffffffu, inv >= 0.f);
-        }
-        uint32_t o[64];
-        tmem_ld_x32(lrow + kColO + ob * 64, o);
-        tmem_ld_x32(lrow + kColO + ob * 64 + 32, o + 32);
-        tmem_wait_ld();
-        tc_fence_before();
-        __syncwarp();
+      const Pass &ps = S.pass[pi % kPasses];
+      if (ps.wait_for > 0) {
+        int w_ok = 1;
         if (lane == 0) {
-          mbar_arrive(&S.o_empty[ob]);
-          if (c == NCH - 1 && q == 0) *reinterpret_cast<volatile int *>(&S.passes_done) = (int)pi;
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {   // 32 channels: rows through the stage, whole sectors out
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            uint32_t pk[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int i = 32 * h + 8 * p + 2 * j;
-              const __nv_bfloat162 bv = __floats2bfloat162_rn(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
-              pk[j] = *reinterpret_cast<const uint32_t *>(&bv);
-            }
-            *reinterpret_cast<uint4 *>(stage + lane * 64 + ((p ^ ((lane >> 1) & 3)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          const volatile int *done = &S.passes_done;
+          uint32_t i = 0;
+          while (*done < ps.wait_for) {
+            if (++i >= kWaitLimit || *abort) { w_ok = 0; *abort = 1; break; }
+            __nanosleep(64);
           }
-          __syncwarp();
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = 8 * i + lane / 4, p = lane % 4;
-            const uint4 v = *reinterpret_cast<const uint4 *>(stage + r * 64 + ((p ^ ((r >> 1) & 3)) << 4));
-            if ((covered >> r) & 1u)
-              reinterpret_cast<uint4 *>(a.out + (size_t)(row0 + r) * D + c * 64 + h * 32)[p] = v;
-          }
-          __syncwarp();
         }
+        ok = __shfl_sync(0xffffffffu, w_ok, 0) != 0;
+        if (!ok) break;
       }
+      bring_rows(ps, pi == 0 ? 8 + kw : kw, pi == 0 ? kFirstWarps : kKeyWarps, pi == 0 ? &S.k_first : &S.k_full[pi & 3u]);
+      if (pi == 0 && lane == 0) mbar_arrive(&S.k_full[0]);   // (its first phase is k_first's: the phases stay in step)
+      free_pass();
+      ++pi;
     }
   }
   // ---- every role is through, or a wait gave up
@@ -583,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
 }
 
 template <int D>
-static cudaError_t launch_t(const DenseAttnArgs &a, int sms, cudaStream_t s) {
+static cudaError_t launch_t(const CUtensorMap &q_map, const DenseAttnArgs &a, int sms, cudaStream_t s) {
   const size_t smem = sizeof(WinSmem<D>) + 1024;
   static_assert(sizeof(WinSmem<D>) + 1024 <= 232448, "shared memory");
   cudaError_t e = cudaFuncSetAttribute(attn_window_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -591,7 +615,7 @@ static cudaError_t launch_t(const DenseAttnArgs &a, int sms, cudaStream_t s) {
   const int rt_own = (a.T_q * a.H + kRows - 1) / kRows;
   const long long units = (long long)a.B * rt_own;
   const int grid = units < sms ? (int)units : sms;
-  return launch_pdl(attn_window_kernel<D>, dim3(grid), dim3(kThreads), smem, s, dim3(1, 1, 1), a, rt_own);
+  return launch_pdl(attn_window_kernel<D>, dim3(grid), dim3(kThreads), smem, s, dim3(1, 1, 1), a, rt_own, q_map);
 }
 
 bool window_fits_ring(const DenseAttnArgs &a) {
@@ -600,11 +624,11 @@ bool window_fits_ring(const DenseAttnArgs &a) {
   return a.n_sink + (a.window > 0 ? a.window + most - 1 : 0) <= ring_keys(a.D);
 }
 
-cudaError_t launch_window_ring(const DenseAttnArgs &a, int sms, cudaStream_t s) {
+cudaError_t launch_window_ring(const CUtensorMap &q_map, const DenseAttnArgs &a, int sms, cudaStream_t s) {
   switch (a.D) {
-    case 128: return launch_t<128>(a, sms, s);
-    case 256: return launch_t<256>(a, sms, s);
-    default: return launch_t<512>(a, sms, s);
+    case 128: return launch_t<128>(q_map, a, sms, s);
+    case 256: return launch_t<256>(q_map, a, sms, s);
+    default: return launch_t<512>(q_map, a, sms, s);
   }
 }
 

@@ -262,7 +262,9 @@ size_t prefix_attn_workspace_bytes(int B, int T_q, int H, int D, int sms);
 cudaError_t launch_prefix_attn(const DenseAttnArgs &a, int sms, cudaStream_t s);
 size_t window_attn_workspace_bytes(int B, int T_q, int H, int D, int window, int n_sink, int sms);
 cudaError_t launch_window_attn(const DenseAttnArgs &a, int sms, cudaStream_t s);
-bool window_fits_ring(const DenseAttnArgs &a);   // the resident form (attn_window.cu) takes it
-cudaError_t launch_window_ring(const DenseAttnArgs &a, int sms, cudaStream_t s);
+// The resident form (attn_window.cu), for the launches it takes; q_map: q as
+// rows of D bf16, boxes of 128 rows x 64 channels in the 128B swizzle.
+bool window_fits_ring(const DenseAttnArgs &a);
+cudaError_t launch_window_ring(const CUtensorMap &q_map, const DenseAttnArgs &a, int sms, cudaStream_t s);
 
 }  // namespace csa2
