@@ -19,15 +19,17 @@
 // of q and the output, 4 bytes per (row, channel), which bounds the kernel (132
 // FLOP per byte at a window of 128 and D 512).
 // Warp roles, all persistent, handing work over through mbarriers:
-//   warps 0-3    softmax, one row per thread, a row's logits in registers; P
-//                replaces S in tensor memory
-//   warps 4-7    O / l -> bf16 -> output, through a per-warp staging tile so that
-//                whole lines are stored
-//   warps 8, 10  tcgen05.mma issuers of S and of O (one lane each)
-//   warp 9       TMA loads of Q, 64 channels at a time
-//   warp 11      scheduler: passes (below) through a ring of three descriptors
-//   warps 12-15  new window rows into the ring (the first pass's, all of a
+//   warps 0-3, 4-7    softmax, one row per thread, each group half of the keys
+//                (they exchange the row maxima); P replaces S in tensor memory
+//   warps 8-11, 12-15  O / l -> bf16 -> output, every other 64-channel block each,
+//                through a per-warp staging tile so that whole sectors are stored
+//   warps 16, 18 tcgen05.mma issuers of S and of O (one lane each)
+//   warp 17      TMA loads of Q, 64 channels at a time
+//   warp 19      scheduler: passes (below) through a ring of three descriptors, and
+//                the new window rows into the ring (the first pass's, a whole
 //                window, by the softmax and output warps too)
+// The three stages of a pass (S, softmax, O) each take about as long as q and the
+// output take from and to memory; two S buffers keep two passes in flight.
 // A pass is a row tile with the range of tokens it needs; a tile whose queries'
 // windows do not fit one range (positions far apart) takes several passes, each
 // storing the rows it covers.  Sinks and window rows enter unscaled; with y =
@@ -43,12 +45,12 @@ namespace csa2 {
 
 namespace {
 
-constexpr int kEpiWarp0 = 4, kMmaWarp = 8, kQWarp = 9, kPvWarp = 10, kSchedWarp = 11, kKeyWarp0 = 12, kKeyWarps = 4;
-constexpr int kThreads = 16 * 32;
-constexpr int kFirstWarps = 12;              // warps that bring the first pass's window rows
-// Registers per thread of the warpgroups (softmax, output, MMA, keys); their
-// sum is at most the launch's 4 x 128.
-constexpr int kRegsSoftmax = 232, kRegsEpi = 112, kRegsMma = 72, kRegsKeys = 96;
+constexpr int kEpiWarp0 = 8, kMmaWarp = 16, kQWarp = 17, kPvWarp = 18, kSchedWarp = 19;
+constexpr int kThreads = 20 * 32;
+constexpr int kFirstWarps = 17;              // warps that bring the first pass's window rows
+// Registers per thread of the warpgroups (2 x softmax, 2 x output, MMA); their
+// sum is at most the launch's 5 x 96.
+constexpr int kRegsSoftmax = 104, kRegsEpi = 88, kRegsMma = 96;
 constexpr int kPasses = 3;                   // descriptors
 constexpr int kOBufs = 3;                    // ring of 64-channel O blocks
 constexpr int kLive = 8;                     // passes that can be unfinished at once (bounded by the rings above)
@@ -76,9 +78,10 @@ struct WinSmem {
   static constexpr int R = ring_keys(D), QSL = q_slots(D);
   alignas(1024) uint8_t kr[(D / 64) * R * 128];     // ring: chunks of [R keys x 128 B]
   alignas(1024) uint8_t q[QSL][kRows * 128];        // Q chunks
-  alignas(16) uint8_t stage[4][32 * 128];           // per output warp: 32 rows x 64 channels bf16
-  float linv[4][kRows];                             // 1 / l of a pass's rows, negative: not covered
-  uint64_t q_full[QSL], q_empty[QSL], k_full[4], k_first, s_full[2], p_full[2], pv_done[2];
+  alignas(16) uint8_t stage[8][32 * 64];            // per output warp: 32 rows x 32 channels bf16
+  float top[2][2][kRows];                           // row maxima of the two halves of the keys, by pass parity
+  float lsum[4][2][kRows];                          // sums of the halves, negative: row not covered
+  uint64_t q_full[QSL], q_empty[QSL], k_full[4], k_first, s_full[2], top_full[2], p_full[2], pv_done[2];
   uint64_t o_full[kOBufs], o_empty[kOBufs], pass_full[kPasses], pass_empty[kPasses], fin;
   uint32_t tmem_base;
   int abort;
@@ -114,12 +117,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
   pdl_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < QSL; ++i) { mbar_init(&S.q_full[i], 1); mbar_init(&S.q_empty[i], 1); }
-    for (int i = 0; i < 4; ++i) mbar_init(&S.k_full[i], kKeyWarps);
+    for (int i = 0; i < 4; ++i) mbar_init(&S.k_full[i], 1);
     mbar_init(&S.k_first, kFirstWarps);
-    for (int i = 0; i < 2; ++i) { mbar_init(&S.s_full[i], 1); mbar_init(&S.p_full[i], 4); mbar_init(&S.pv_done[i], 1); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&S.s_full[i], 1); mbar_init(&S.top_full[i], 8); mbar_init(&S.p_full[i], 8); mbar_init(&S.pv_done[i], 1); }
     for (int i = 0; i < kOBufs; ++i) { mbar_init(&S.o_full[i], 1); mbar_init(&S.o_empty[i], 4); }
-    // readers of a descriptor: key, softmax and output warps, S, O, Q
-    for (int i = 0; i < kPasses; ++i) { mbar_init(&S.pass_full[i], 1); mbar_init(&S.pass_empty[i], kKeyWarps + 4 + 4 + 3); }
+    // readers of a descriptor: softmax and output warps, S, O, Q
+    for (int i = 0; i < kPasses; ++i) { mbar_init(&S.pass_full[i], 1); mbar_init(&S.pass_empty[i], 8 + 8 + 3); }
     mbar_init(&S.fin, 2);
     S.abort = 0;
     S.passes_done = 0;
@@ -211,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
   if (warp < kEpiWarp0) {
     // ================================================ softmax: thread = row
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-    const int q = warp & 3, row = 32 * q + lane;
+    const int q = warp & 3, part = warp >> 2, row = 32 * q + lane;
     const uint32_t lrow = tmem + ((uint32_t)(32 * q) << 16);
     // y = log2(weight x key scale) = S x l + o, with the sign of the softmax
     // scale taken into S and the factor never 0, so that a hidden key's -inf stays
@@ -246,29 +249,40 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
       ok = all_wait(&S.s_full[buf], (pi >> 1) & 1u);
       if (!ok) break;
       tc_fence_after();
-      uint32_t sv[NW * 32];   // (what a last word of 16 reads behind the ring's keys has no bit set)
-#pragma unroll
-      for (int w = 0; w < NW; ++w) tmem_ld_x32(scol + 32 * w, sv + 32 * w);
-      tmem_wait_ld();
-      float top = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        const uint32_t seen = seen_word(w);
-        uint32_t *x = sv + 32 * w;
-        if (a.scale < 0.f) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) x[j] ^= 0x80000000u;
-        }
-        if (32 * w < n_sink) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (32 * w + j < n_sink) x[j] = __float_as_uint(fmaf(__uint_as_float(x[j]), s2w, o2w));
-        }
+      // words of 32 keys, [w0, w0 + nw) by this warp; S is read twice (the
+      // code of a word is a loop's body: straight-line code for all of them is
+      // fetched from L2 every pass).  What a last word of 16 reads behind the
+      // ring's keys has no bit set.
+      constexpr int HALF = (NW + 1) / 2;
+      const int w0 = part * HALF, w_end = part ? NW : HALF;
+      auto hide = [&](uint32_t seen, uint32_t *x) {
         if (!__all_sync(0xffffffffu, seen == 0xFFFFFFFFu)) {
 #pragma unroll
           for (int j = 0; j < 32; ++j)
             if (!((seen >> j) & 1u)) x[j] = 0xFF800000u;
         }
+      };
+      auto logits = [&](int w, uint32_t *x) {   // a row's S of word w, to be multiplied by lw; hidden: -inf
+        tmem_ld_x32(scol + 32 * w, x);
+        const uint32_t seen = seen_word(w), sinks = span(w, 0, n_sink);
+        tmem_wait_ld();
+        if (a.scale < 0.f) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[j] ^= 0x80000000u;
+        }
+        if (sinks) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if ((sinks >> j) & 1u) x[j] = __float_as_uint(fmaf(__uint_as_float(x[j]), s2w, o2w));
+        }
+        hide(seen, x);
+        return sinks;
+      };
+      float top = -INFINITY;
+#pragma unroll 1
+      for (int w = w0; w < w_end; ++w) {
+        uint32_t x[32];
+        logits(w, x);
         float m4[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) m4[j] = __uint_as_float(x[j]);
@@ -276,28 +290,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
         for (int j = 4; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], __uint_as_float(x[j]));
         top = fmaxf(top, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
       }
+      S.top[buf][part][row] = top;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.top_full[buf]);
+      ok = all_wait(&S.top_full[buf], (pi >> 1) & 1u);
+      if (!ok) break;
+      top = fmaxf(top, S.top[buf][part ^ 1][row]);
       // P = 2^(y - max y) = hi + lo, in place (columns [0, 16) and [16, 32) of
       // the word's 32), and the sums of the two sorts of keys
       const float mu = top == -INFINITY ? 0.f : top * lw;
       float sum_s = 0.f;
       uint64_t sum2 = 0;
       const uint64_t l2 = f32x2(lw, lw), m2 = f32x2(-mu, -mu);
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        uint32_t pr[32];
+#pragma unroll 1
+      for (int w = w0; w < w_end; ++w) {
+        uint32_t x[32], pr[32];
+        const uint32_t sinks = logits(w, x);
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
-          const uint32_t *x = sv + 32 * w + j;
-          const float2 y = unpack_f32x2(fma_f32x2(f32x2(__uint_as_float(x[0]), __uint_as_float(x[1])), l2, m2));
+          const float2 y = unpack_f32x2(fma_f32x2(f32x2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])), l2, m2));
           const float p0 = ex2_approx(y.x), p1 = ex2_approx(y.y);
-          float w0 = p0, w1 = p1;
-          if (32 * w < n_sink) {   // (a word with sinks)
-            const bool k0 = 32 * w + j < n_sink, k1 = 32 * w + j + 1 < n_sink;
-            sum_s += (k0 ? p0 : 0.f) + (k1 ? p1 : 0.f);
-            w0 = k0 ? 0.f : p0;
-            w1 = k1 ? 0.f : p1;
-          }
-          sum2 = add_f32x2(sum2, f32x2(w0, w1));
+          x[j] = __float_as_uint(p0);
+          x[j + 1] = __float_as_uint(p1);
           const __nv_bfloat162 hv = __floats2bfloat162_rn(p0, p1);
           const uint32_t hi = *reinterpret_cast<const uint32_t *>(&hv);
           const __nv_bfloat162 lv = __floats2bfloat162_rn(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xFFFF0000u));
@@ -305,11 +319,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
           pr[16 + j / 2] = *reinterpret_cast<const uint32_t *>(&lv);
         }
         tmem_st_x32(scol + 32 * w, pr);
+        if (sinks) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const bool k = (sinks >> j) & 1u;
+            sum_s += k ? __uint_as_float(x[j]) : 0.f;
+            x[j] = k ? 0u : x[j];
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) sum2 = add_f32x2(sum2, f32x2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])));
       }
       const float2 st2 = unpack_f32x2(sum2);
-      const float sum_w = st2.x + st2.y;
-      const float l = sum_s * rs_s + sum_w * rs_w;
-      S.linv[pi & 3u][row] = mine ? (l > 0.f ? 1.f / l : 0.f) : -1.f;
+      S.lsum[pi & 3u][part][row] = mine ? sum_s * rs_s + (st2.x + st2.y) * rs_w : -1.f;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -322,25 +344,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsEpi));
     const int q = warp & 3;
     const uint32_t lrow = tmem + ((uint32_t)(32 * q) << 16);
-    uint8_t *stage = S.stage[q];
+    const uint32_t part = (warp - kEpiWarp0) >> 2;
+    uint8_t *stage = S.stage[warp - kEpiWarp0];
     uint32_t oi = 0;
     bool ok = true;
     while (ok && next_pass()) {
       const int row0 = S.pass[pi % kPasses].row0 + 32 * q;
-      if (pi == 0) bring_rows(S.pass[0], 4 + q, kFirstWarps, &S.k_first);
+      if (pi == 0) bring_rows(S.pass[0], warp, kFirstWarps, &S.k_first);
       free_pass();
       ++pi;   // (passes done when this one is)
       float inv = -1.f;
       uint32_t covered = 0;
+      oi += part;
 #pragma unroll 1
-      for (int c = 0; c < NCH; ++c) {
+      for (int c = (int)part; c < NCH; c += 2) {
         const uint32_t ob = oi % kOBufs;
         ok = all_wait(&S.o_full[ob], (oi / kOBufs) & 1u);
         if (!ok) break;
-        ++oi;
+        oi += 2;
         tc_fence_after();
-        if (c == 0) {   // the O product follows the softmax: its sums are there
-          inv = S.linv[(pi - 1) & 3u][32 * q + lane];
+        if (c == (int)part) {   // the O product follows the softmax: its sums are there
+          const float l0 = S.lsum[(pi - 1) & 3u][0][32 * q + lane], l = l0 + S.lsum[(pi - 1) & 3u][1][32 * q + lane];
+          inv = l0 < 0.f ? -1.f : (l > 0.f ? 1.f / l : 0.f);
           covered = __ballot_sync(0xffffffffu, inv >= 0.f);
         }
         uint32_t o[64];
@@ -353,31 +378,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
           mbar_arrive(&S.o_empty[ob]);
           if (c == NCH - 1 && q == 0) *reinterpret_cast<volatile int *>(&S.passes_done) = (int)pi;
         }
-        // rows through the stage, whole lines out
 #pragma unroll
-        for (int p = 0; p < 8; ++p) {
-          uint32_t pk[4];
+        for (int h = 0; h < 2; ++h) {   // 32 channels: rows through the stage, whole sectors out
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int i = 8 * p + 2 * j;
-            const __nv_bfloat162 bv = __floats2bfloat162_rn(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
-            pk[j] = *reinterpret_cast<const uint32_t *>(&bv);
+          for (int p = 0; p < 4; ++p) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int i = 32 * h + 8 * p + 2 * j;
+              const __nv_bfloat162 bv = __floats2bfloat162_rn(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
+              pk[j] = *reinterpret_cast<const uint32_t *>(&bv);
+            }
+            *reinterpret_cast<uint4 *>(stage + lane * 64 + ((p ^ ((lane >> 1) & 3)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
           }
-          *reinterpret_cast<uint4 *>(stage + lane * 128 + ((p ^ (lane & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-        }
-        __syncwarp();
+          __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 4 * i + lane / 8, p = lane % 8;
-          const uint4 v = *reinterpret_cast<const uint4 *>(stage + r * 128 + ((p ^ (r & 7)) << 4));
-          if ((covered >> r) & 1u) reinterpret_cast<uint4 *>(a.out + (size_t)(row0 + r) * D + c * 64)[p] = v;
+          for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + lane / 4, p = lane % 4;
+            const uint4 v = *reinterpret_cast<const uint4 *>(stage + r * 64 + ((p ^ ((r >> 1) & 3)) << 4));
+            if ((covered >> r) & 1u) reinterpret_cast<uint4 *>(a.out + (size_t)(row0 + r) * D + c * 64 + h * 32)[p] = v;
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
+      oi -= part;   // (the pass's blocks are counted by both)
     }
-  } else if (warp < kKeyWarp0) {
-    // ================================================ scheduler, MMA issuers, Q
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsMma));
+  } else {
+    // ================================================ scheduler and window rows, MMA issuers, Q
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMma));
     if (warp == kSchedWarp) {
       const int units = a.B * rt_own, rows = a.T_q * a.H;
       const int u_end = (int)((long long)units * (blockIdx.x + 1) / gridDim.x);
@@ -462,6 +490,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&S.pass_full[pi % kPasses]);
+          if (more) {
+            const Pass &pr = S.pass[pi % kPasses];
+            if (pr.wait_for > 0) {
+              int w_ok = 1;
+              if (lane == 0) {
+                const volatile int *done = &S.passes_done;
+                uint32_t i = 0;
+                while (*done < pr.wait_for) {
+                  if (++i >= kWaitLimit || *abort) { w_ok = 0; *abort = 1; break; }
+                  __nanosleep(64);
+                }
+              }
+              ok = __shfl_sync(0xffffffffu, w_ok, 0) != 0;
+              if (!ok) break;
+            }
+            if (pi == 0) bring_rows(pr, kFirstWarps - 1, kFirstWarps, &S.k_first);
+            else bring_rows(pr, 0, 1, &S.k_full[pi & 3u]);
+            if (pi == 0 && lane == 0) mbar_arrive(&S.k_full[0]);   // (its first phase is k_first's: the phases stay in step)
+          }
           ++pi;
         } while (more && from != INT_MAX);
         if (!more) break;
@@ -559,31 +606,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
         }
       }
       __syncwarp();
-    }
-  } else {
-    // ================================================ window rows
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsKeys));
-    const int kw = warp - kKeyWarp0;
-    bool ok = true;
-    while (ok && next_pass()) {
-      const Pass &ps = S.pass[pi % kPasses];
-      if (ps.wait_for > 0) {
-        int w_ok = 1;
-        if (lane == 0) {
-          const volatile int *done = &S.passes_done;
-          uint32_t i = 0;
-          while (*done < ps.wait_for) {
-            if (++i >= kWaitLimit || *abort) { w_ok = 0; *abort = 1; break; }
-            __nanosleep(64);
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, w_ok, 0) != 0;
-        if (!ok) break;
-      }
-      bring_rows(ps, pi == 0 ? 8 + kw : kw, pi == 0 ? kFirstWarps : kKeyWarps, pi == 0 ? &S.k_first : &S.k_full[pi & 3u]);
-      if (pi == 0 && lane == 0) mbar_arrive(&S.k_full[0]);   // (its first phase is k_first's: the phases stay in step)
-      free_pass();
-      ++pi;
     }
   }
   // ---- every role is through, or a wait gave up
