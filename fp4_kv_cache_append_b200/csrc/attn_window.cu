@@ -26,8 +26,8 @@
 //   warps 16, 18 tcgen05.mma issuers of S and of O (one lane each)
 //   warp 17      TMA loads of Q, 64 channels at a time
 //   warp 19      scheduler: passes (below) through a ring of three descriptors, and
-//                the new window rows into the ring (the first pass's, a whole
-//                window, by the softmax and output warps too)
+//                the new window rows into the ring (a whole window, when the ring
+//                starts anew, by the softmax and output warps too)
 // The three stages of a pass (S, softmax, O) each take about as long as q and the
 // output take from and to memory; two S buffers keep two passes in flight.
 // A pass is a row tile with the range of tokens it needs; a tile whose queries'
@@ -47,7 +47,7 @@ namespace {
 
 constexpr int kEpiWarp0 = 8, kMmaWarp = 16, kQWarp = 17, kPvWarp = 18, kSchedWarp = 19;
 constexpr int kThreads = 20 * 32;
-constexpr int kFirstWarps = 17;              // warps that bring the first pass's window rows
+constexpr int kColdWarps = 17;               // warps that bring a whole window's rows
 // Registers per thread of the warpgroups (2 x softmax, 2 x output, MMA); their
 // sum is at most the launch's 5 x 96.
 constexpr int kRegsSoftmax = 104, kRegsEpi = 88, kRegsMma = 96;
@@ -56,7 +56,7 @@ constexpr int kOBufs = 3;                    // ring of 64-channel O blocks
 constexpr int kLive = 8;                     // passes that can be unfinished at once (bounded by the rings above)
 constexpr uint32_t kTmemCols = 512;
 
-// Keys that the ring holds (N of S): 144 KB at D 512; 64-channel chunks of Q in flight.
+// Most keys that a ring holds (144 KB at D 512); 64-channel chunks of Q in flight.
 __host__ __device__ constexpr int ring_keys(int D) { return D == 512 ? 144 : 160; }
 __host__ __device__ constexpr int q_slots(int D) { return D == 512 ? 3 : 4; }
 
@@ -70,18 +70,19 @@ struct Pass {
   int load_lo;             // window rows [load_lo, end) enter the ring
   int load_sinks;          // a new sequence: its sinks enter too
   int wait_for;            // passes that must be complete before the rows enter
+  int cold;                // > 0: the ring starts anew (the how-manieth time), all warps bring rows
   int pos[kMaxQ];
 };
 
 template <int D>
 struct WinSmem {
-  static constexpr int R = ring_keys(D), QSL = q_slots(D);
-  alignas(1024) uint8_t kr[(D / 64) * R * 128];     // ring: chunks of [R keys x 128 B]
+  static constexpr int QSL = q_slots(D);
+  alignas(1024) uint8_t kr[(D / 64) * ring_keys(D) * 128];     // ring: chunks of [R keys x 128 B]
   alignas(1024) uint8_t q[QSL][kRows * 128];        // Q chunks
   alignas(16) uint8_t stage[8][32 * 64];            // per output warp: 32 rows x 32 channels bf16
   float top[2][2][kRows];                           // row maxima of the two halves of the keys, by pass parity
   float lsum[4][2][kRows];                          // sums of the halves, negative: row not covered
-  uint64_t q_full[QSL], q_empty[QSL], k_full[4], k_first, s_full[2], top_full[2], p_full[2], pv_done[2];
+  uint64_t q_full[QSL], q_empty[QSL], k_full[4], k_cold, s_full[2], top_full[2], p_full[2], pv_done[2];
   uint64_t o_full[kOBufs], o_empty[kOBufs], pass_full[kPasses], pass_empty[kPasses], fin;
   uint32_t tmem_base;
   int abort;
@@ -104,10 +105,10 @@ __device__ __forceinline__ uint32_t no_nan(uint32_t w) {
 }  // namespace
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAttnArgs a, const int rt_own,
+__global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAttnArgs a, const int rt_own, const int R,
                                                                   const __grid_constant__ CUtensorMap q_map) {
-  constexpr int R = ring_keys(D), QSL = q_slots(D), NCH = D / 64;
-  constexpr uint32_t kIdS = mma_idesc(kRows, R, 1u, 1u);
+  constexpr int QSL = q_slots(D), NCH = D / 64;
+  const uint32_t id_s = mma_idesc(kRows, R, 1u, 1u);   // N = R keys, a multiple of 16
   constexpr uint32_t kIdO = mma_idesc(kRows, 64, 1u, 1u) | (1u << 16);   // B (V) MN-major
   extern __shared__ uint8_t smem_raw[];
   WinSmem<D> &S = *reinterpret_cast<WinSmem<D> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
   if (tid == 0) {
     for (int i = 0; i < QSL; ++i) { mbar_init(&S.q_full[i], 1); mbar_init(&S.q_empty[i], 1); }
     for (int i = 0; i < 4; ++i) mbar_init(&S.k_full[i], 1);
-    mbar_init(&S.k_first, kFirstWarps);
+    mbar_init(&S.k_cold, kColdWarps);
     for (int i = 0; i < 2; ++i) { mbar_init(&S.s_full[i], 1); mbar_init(&S.top_full[i], 8); mbar_init(&S.p_full[i], 8); mbar_init(&S.pv_done[i], 1); }
     for (int i = 0; i < kOBufs; ++i) { mbar_init(&S.o_full[i], 1); mbar_init(&S.o_empty[i], 4); }
     // readers of a descriptor: softmax and output warps, S, O, Q
@@ -207,6 +208,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
   };
+  // Until `n` passes are complete (their O products: nothing reads their keys any more).
+  auto wait_done = [&](int n) -> bool {
+    int w_ok = 1;
+    if (n > 0 && lane == 0) {
+      const volatile int *done = &S.passes_done;
+      uint32_t i = 0;
+      while (*done < n) {
+        if (++i >= kWaitLimit || *abort) { w_ok = 0; *abort = 1; break; }
+        __nanosleep(64);
+      }
+    }
+    return __shfl_sync(0xffffffffu, w_ok, 0) != 0;
+  };
   auto all_wait = [&](uint64_t *bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort)) != 0;
   };
@@ -225,7 +239,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
     bool ok = true;
     while (ok && next_pass()) {
       const Pass &ps = S.pass[pi % kPasses];
-      if (pi == 0) bring_rows(ps, warp, kFirstWarps, &S.k_first);
+      if (ps.cold) {
+        ok = wait_done(ps.wait_for);
+        if (!ok) break;
+        bring_rows(ps, warp, kColdWarps, &S.k_cold);
+      }
       const int frow = ps.row0 + row;
       const bool live = row < ps.nrows;
       const int t = live ? ps.pos[frow / a.H - ps.q0] : -1;
@@ -234,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
       // the slots this row sees, one bit per key
       int wlo = a.window > 0 ? t - a.window + 1 : t + 1;
       if (wlo < 0) wlo = 0;
-      constexpr int NW = (R + 31) / 32;
+      const int NW = (R + 31) / 32;
       const int len = mine && t >= 0 && a.window > 0 ? t - wlo + 1 : 0;
       const int s0 = n_sink + wlo % rw, e0 = s0 + len;              // [s0, e0), wrapping from R to n_sink
       const int e1 = e0 < R ? e0 : R, w1 = e0 > R ? n_sink + e0 - R : n_sink;
@@ -253,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
       // code of a word is a loop's body: straight-line code for all of them is
       // fetched from L2 every pass).  What a last word of 16 reads behind the
       // ring's keys has no bit set.
-      constexpr int HALF = (NW + 1) / 2;
+      const int HALF = (NW + 1) / 2;
       const int w0 = part * HALF, w_end = part ? NW : HALF;
       auto hide = [&](uint32_t seen, uint32_t *x) {
         if (!__all_sync(0xffffffffu, seen == 0xFFFFFFFFu)) {
@@ -350,7 +368,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
     bool ok = true;
     while (ok && next_pass()) {
       const int row0 = S.pass[pi % kPasses].row0 + 32 * q;
-      if (pi == 0) bring_rows(S.pass[0], warp, kFirstWarps, &S.k_first);
+      if (S.pass[pi % kPasses].cold) {
+        ok = wait_done(S.pass[pi % kPasses].wait_for);
+        if (!ok) break;
+        bring_rows(S.pass[pi % kPasses], warp, kColdWarps, &S.k_cold);
+      }
       free_pass();
       ++pi;   // (passes done when this one is)
       float inv = -1.f;
@@ -410,6 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
       const int units = a.B * rt_own, rows = a.T_q * a.H;
       const int u_end = (int)((long long)units * (blockIdx.x + 1) / gridDim.x);
       int u = (int)((long long)units * blockIdx.x / gridDim.x);
+      int cold = 0;                                    // times that the ring started anew
       int res_b = -1, res_lo = 0, res_hi = 0;          // ring: tokens [res_lo, res_hi) of sequence res_b
       int old[kLive];                                  // first token of the last passes (newest first)
 #pragma unroll
@@ -460,13 +483,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
             } else {
               lo = 0;
             }
-            // rows that enter: behind what the ring holds, or all of them
-            const bool same = b == res_b && lo >= res_lo && lo <= res_hi;
+            // rows that enter: behind what the ring holds, or all of them (padded queries alone: none)
+            const bool none = end == 0;
+            const bool same = none || (b == res_b && lo >= res_lo && lo <= res_hi);
             int load_lo = same ? (res_hi < end ? res_hi : end) : lo;
-            if (a.window <= 0) load_lo = end;
+            if (a.window <= 0 || none) load_lo = end;
             int wait_for = 0;
-            if (b != res_b || !same) {
+            if (!same) {
               wait_for = (int)pi;
+              ++cold;
             } else if (end > load_lo) {
               // slots of tokens below end - rw are overwritten: every unfinished pass that needs one of them
 #pragma unroll
@@ -476,15 +501,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
             if (lane == 0) {
               ps.more = 1; ps.row0 = row0; ps.nrows = nrows; ps.b = b; ps.q0 = q0; ps.nq = nq;
               ps.lo = lo; ps.end = end; ps.from = from; ps.first = first;
-              ps.load_lo = load_lo; ps.load_sinks = b != res_b; ps.wait_for = wait_for;
+              ps.load_lo = load_lo; ps.load_sinks = !none && b != res_b; ps.wait_for = wait_for;
+              ps.cold = same ? 0 : cold;
             }
 #pragma unroll
             for (int i = kLive - 1; i > 0; --i) old[i] = old[i - 1];
             old[0] = end > lo ? lo : INT_MAX;
             if (!same) { res_lo = lo; res_hi = lo; }
-            res_b = b;
-            res_hi = end > res_hi ? end : res_hi;
-            if (res_lo < res_hi - rw) res_lo = res_hi - rw;
+            if (!none) {
+              res_b = b;
+              res_hi = end > res_hi ? end : res_hi;
+              if (res_lo < res_hi - rw) res_lo = res_hi - rw;
+            }
             from = next == INT_MAX ? INT_MAX : end;
             first = 0;
           }
@@ -492,22 +520,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
           if (lane == 0) mbar_arrive(&S.pass_full[pi % kPasses]);
           if (more) {
             const Pass &pr = S.pass[pi % kPasses];
-            if (pr.wait_for > 0) {
-              int w_ok = 1;
-              if (lane == 0) {
-                const volatile int *done = &S.passes_done;
-                uint32_t i = 0;
-                while (*done < pr.wait_for) {
-                  if (++i >= kWaitLimit || *abort) { w_ok = 0; *abort = 1; break; }
-                  __nanosleep(64);
-                }
-              }
-              ok = __shfl_sync(0xffffffffu, w_ok, 0) != 0;
-              if (!ok) break;
+            ok = wait_done(pr.wait_for);
+            if (!ok) break;
+            if (pr.cold) {
+              bring_rows(pr, kColdWarps - 1, kColdWarps, &S.k_cold);
+              if (lane == 0) mbar_arrive(&S.k_full[pi & 3u]);   // (k_full's phases stay in step with the passes)
+            } else {
+              bring_rows(pr, 0, 1, &S.k_full[pi & 3u]);
             }
-            if (pi == 0) bring_rows(pr, kFirstWarps - 1, kFirstWarps, &S.k_first);
-            else bring_rows(pr, 0, 1, &S.k_full[pi & 3u]);
-            if (pi == 0 && lane == 0) mbar_arrive(&S.k_full[0]);   // (its first phase is k_first's: the phases stay in step)
           }
           ++pi;
         } while (more && from != INT_MAX);
@@ -523,9 +543,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
         while (ok) {
           ok = wait_or_abort(&S.pass_full[pi % kPasses], (pi / kPasses) & 1u, abort);
           if (!ok || !S.pass[pi % kPasses].more) break;
+          const int cold = S.pass[pi % kPasses].cold;
           mbar_arrive(&S.pass_empty[pi % kPasses]);
           const uint32_t buf = pi & 1u, scol = tmem + kColS + buf * kSCols;
-          ok = pi == 0 ? wait_or_abort(&S.k_first, 0, abort) : wait_or_abort(&S.k_full[pi & 3u], (pi >> 2) & 1u, abort);
+          ok = wait_or_abort(&S.k_full[pi & 3u], (pi >> 2) & 1u, abort);
+          if (ok && cold) ok = wait_or_abort(&S.k_cold, (cold - 1) & 1, abort);
           if (ok && pi >= 2) ok = wait_or_abort(&S.pv_done[buf], ((pi >> 1) & 1u) ^ 1u, abort);   // the buffer's last P has been used
           if (!ok) break;
 #pragma unroll 1
@@ -539,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
             const uint64_t db = smem_desc_kmajor(smem_u32(S.kr) + c * (R * 128), 128);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              tc_mma_f16(scol, da + ((kk * 32) >> 4), db + ((kk * 32) >> 4), kIdS, (c > 0 || kk > 0) ? 1u : 0u);
+              tc_mma_f16(scol, da + ((kk * 32) >> 4), db + ((kk * 32) >> 4), id_s, (c > 0 || kk > 0) ? 1u : 0u);
             tc_commit(&S.q_empty[slot]);
           }
           if (!ok) break;
@@ -592,12 +614,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
             ++oi;
             tc_fence_after();
             const uint64_t dv = smem_desc_mnmajor_sw128(smem_u32(S.kr) + c * (R * 128), R * 128, 1024);
+#pragma unroll 1
+            for (int w = 0; 32 * w < R; ++w)   // a word's two steps of 16 keys, hi and lo of each
 #pragma unroll
-            for (int ks = 0; ks < R / 16; ++ks)
-#pragma unroll
-              for (int lo = 0; lo < 2; ++lo)
-                tc_mma_f16_ta(tmem + kColO + ob * 64, pcol + 32 * (ks / 2) + 8 * (ks % 2) + 16 * lo,
-                              dv + ((2 * ks * 1024) >> 4), kIdO, (ks > 0 || lo > 0) ? 1u : 0u);
+              for (int k = 0; k < 4; ++k)
+                if (32 * w + 16 * (k / 2) < R)
+                  tc_mma_f16_ta(tmem + kColO + ob * 64, pcol + 32 * w + 8 * (k / 2) + 16 * (k % 2),
+                                dv + (uint64_t)((w * 4096 + (k / 2) * 2048) >> 4), kIdO, (w > 0 || k > 0) ? 1u : 0u);
             tc_commit(&S.o_full[ob]);
           }
           if (!ok) break;
@@ -628,6 +651,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
   }
 }
 
+// Queries that 128 rows can touch.
+static int tile_queries(const DenseAttnArgs &a) {
+  const int nq = (kRows - 1 + a.H - 1) / a.H + 1;
+  return a.T_q < nq ? a.T_q : nq;
+}
+
 template <int D>
 static cudaError_t launch_t(const CUtensorMap &q_map, const DenseAttnArgs &a, int sms, cudaStream_t s) {
   const size_t smem = sizeof(WinSmem<D>) + 1024;
@@ -637,13 +666,15 @@ static cudaError_t launch_t(const CUtensorMap &q_map, const DenseAttnArgs &a, in
   const int rt_own = (a.T_q * a.H + kRows - 1) / kRows;
   const long long units = (long long)a.B * rt_own;
   const int grid = units < sms ? (int)units : sms;
-  return launch_pdl(attn_window_kernel<D>, dim3(grid), dim3(kThreads), smem, s, dim3(1, 1, 1), a, rt_own, q_map);
+  // the keys of a tile, and room for the rows of the next two while a tile's are in use
+  const int most = tile_queries(a), need = a.n_sink + (a.window > 0 ? a.window + most - 1 : 0);
+  int R = (need + 2 * most + 15) / 16 * 16;
+  if (R > ring_keys(D)) R = ring_keys(D);
+  return launch_pdl(attn_window_kernel<D>, dim3(grid), dim3(kThreads), smem, s, dim3(1, 1, 1), a, rt_own, R, q_map);
 }
 
 bool window_fits_ring(const DenseAttnArgs &a) {
-  const int nq = (kRows - 1 + a.H - 1) / a.H + 1;   // queries that 128 rows can touch
-  const int most = a.T_q < nq ? a.T_q : nq;
-  return a.n_sink + (a.window > 0 ? a.window + most - 1 : 0) <= ring_keys(a.D);
+  return a.n_sink + (a.window > 0 ? a.window + tile_queries(a) - 1 : 0) <= ring_keys(a.D);
 }
 
 cudaError_t launch_window_ring(const CUtensorMap &q_map, const DenseAttnArgs &a, int sms, cudaStream_t s) {
