@@ -132,19 +132,32 @@ def _check_device(device, what: str):
         raise ValueError(f"{what} must be on the current device cuda:{cur} (got one on {device})")
 
 
+# The current stream as a plain integer: marshalling is a visible part of the
+# smallest calls, and the public form builds a stream object (3 us).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _elsewhere(device) -> bool:
+    """Whether a tensor's device needs the full check (_check_device)."""
+    return _device_required() and device.index != torch.cuda.current_device()
+
+
 def _ptr(t: torch.Tensor | None, dtype=None):
     if t is None:
         return None
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"expected {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
-    _check_device(t.device, "tensors")
+    if _elsewhere(t.device):
+        _check_device(t.device, "tensors")
     return t.data_ptr()
 
 
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None and _device_required():
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
@@ -170,7 +183,8 @@ class MainCache:
         object.__setattr__(self, "_desc", None)
 
     def desc(self) -> MainCacheDesc:
-        _check_device(self.codes.device, "the cache's planes")
+        if _elsewhere(self.codes.device):
+            _check_device(self.codes.device, "the cache's planes")
         if self._desc is None:
             object.__setattr__(self, "_desc", MainCacheDesc(
                 self.codes.data_ptr(), self.scales.data_ptr(), self.ik.data_ptr(), self.ik_scale.data_ptr(),
@@ -207,7 +221,8 @@ class SwaCache:
         object.__setattr__(self, "_desc", None)
 
     def desc(self) -> SwaCacheDesc:
-        _check_device(self.rows.device, "the window cache's rows")
+        if _elsewhere(self.rows.device):
+            _check_device(self.rows.device, "the window cache's rows")
         if self._desc is None:
             object.__setattr__(self, "_desc", SwaCacheDesc(self.rows.data_ptr(), self.scale, self.B, self.W_cap,
                                                            self.D, self.window))
@@ -250,7 +265,8 @@ class PagePool:
         object.__setattr__(self, "_desc", None)
 
     def desc(self) -> PagePoolDesc:
-        _check_device(self.codes.device, "the pool's planes")
+        if _elsewhere(self.codes.device):
+            _check_device(self.codes.device, "the pool's planes")
         if self._desc is None:
             object.__setattr__(self, "_desc", PagePoolDesc(
                 self.codes.data_ptr(), self.scales.data_ptr(), self.refs.data_ptr(), self.table.data_ptr(),

@@ -1181,7 +1181,8 @@ template <int D, int MODE>
 cudaError_t launch_dense(const DenseAttnArgs &a, const Schedule &sc, cudaStream_t s) {
   const size_t smem = sizeof(DenseSmem<D>) + 1024;
   static_assert(sizeof(DenseSmem<D>) + 1024 <= 232448, "shared memory");
-  cudaError_t e = cudaFuncSetAttribute(attn_dense_kernel<D, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem_once(attn_dense_kernel<D, MODE>, smem, &allowed);
   if (e != cudaSuccess) return e;
   return launch_pdl(attn_dense_kernel<D, MODE>, dim3(sc.grid), dim3(kThreads), smem, s, dim3(1, 1, 1), a, sc);
 }

@@ -3,6 +3,8 @@
 #pragma once
 #include <limits.h>
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace csa2 {
@@ -57,6 +59,18 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t *bar, uint32_t parity, vo
   }
   *abort = 1;
   return false;
+}
+
+// Raises a kernel's dynamic shared memory limit, once per device (bit d of
+// `done`; the attribute belongs to the device's context).
+template <typename K>
+inline cudaError_t allow_smem_once(K kernel, size_t smem, std::atomic<uint64_t> *done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 64 && ((done->load(std::memory_order_relaxed) >> dev) & 1u))) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess && dev < 64) done->fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
+  return e;
 }
 
 }  // namespace csa2

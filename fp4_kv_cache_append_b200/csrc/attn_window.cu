@@ -661,7 +661,8 @@ template <int D>
 static cudaError_t launch_t(const CUtensorMap &q_map, const DenseAttnArgs &a, int sms, cudaStream_t s) {
   const size_t smem = sizeof(WinSmem<D>) + 1024;
   static_assert(sizeof(WinSmem<D>) + 1024 <= 232448, "shared memory");
-  cudaError_t e = cudaFuncSetAttribute(attn_window_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem_once(attn_window_kernel<D>, smem, &allowed);
   if (e != cudaSuccess) return e;
   const int rt_own = (a.T_q * a.H + kRows - 1) / kRows;
   const long long units = (long long)a.B * rt_own;
