@@ -128,6 +128,23 @@ csa2_status encode_bf16_map(const void *base, int64_t rows, int64_t cols, int bo
   return CSA2_OK;
 }
 
+// 2D map over a plane of bytes [rows][cols], boxes of box_rows x box_cols.
+csa2_status encode_u8_map(const void *base, int64_t rows, int cols, int box_rows, int box_cols, CUtensorMapSwizzle swizzle,
+                          CUtensorMap *map) {
+  EncodeTiled enc = nullptr;
+  csa2_status st = get_encoder(&enc);
+  if (st != CSA2_OK) return st;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)cols};
+  cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(CSA2_ERR_INVALID_ARG, "cuTensorMapEncodeTiled (bytes) failed (%d)", (int)r);
+  return CSA2_OK;
+}
+
 csa2_status check_main(const csa2_main_cache *m, bool need_pending) {
   if (!m) return fail(CSA2_ERR_INVALID_ARG, "main cache is NULL");
   if (!m->codes || !m->scales || !m->ik || !m->ik_scale || !m->n_entries)
@@ -733,7 +750,16 @@ csa2_status csa2_prefix_attn_decode(const csa2_page_pool *pool, const int32_t *s
   }
   a.q = q; a.q_pos = q_pos; a.B = B; a.T_q = T_q; a.H = H; a.D = pool->D;
   a.scale = softmax_scale; a.out = out; a.ws = ws; a.status = d->status;
-  cudaError_t e = launch_prefix_attn(a, d->sms, reinterpret_cast<cudaStream_t>(stream));
+  const int box = prefix_attn_box(pool->page), D = pool->D, DO = D < 256 ? D : 256;
+  const int64_t rows = (int64_t)pool->n_pages * pool->page;
+  const int join = D == 128 ? 2 : 1;   // entries whose scales make a row of 16 bytes or more
+  CUtensorMap codes, scales;
+  if ((st = encode_u8_map(pool->codes, rows, D / 2, box, DO / 2,
+                          D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, &codes)) != CSA2_OK ||
+      (st = encode_u8_map(pool->scales, rows / join, D / 16 * join, box / join, 16, CU_TENSOR_MAP_SWIZZLE_NONE,
+                          &scales)) != CSA2_OK)
+    return st;
+  cudaError_t e = launch_prefix_attn(codes, scales, a, d->sms, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? CSA2_OK : cuda_fail(e, "prefix attention launch");
 }
 

@@ -66,8 +66,9 @@ constexpr int kRegsFetch = 88, kRegsSoftmax = 208, kRegsMma = 128;
 constexpr int kLoadWarp = 13;                // loader: lane = keys lane and lane + 32
 constexpr int kPvWarp = 14;                  // MMA issuer of O (kMmaWarp: of S)
 constexpr int kStages = 3;                   // raw steps in flight or in use
-// A stage: 64 rows of 128 bytes (codes, or FP8 values), then 64 x 16 of scales.
-constexpr int kRawRow = 128, kRawSc = kTile * kRawRow, kRawScRow = 16, kRawBytes = kRawSc + kTile * kRawScRow;
+// A stage: 64 rows of 128 bytes (codes, 64 bytes for D 128, or FP8 values),
+// then 64 rows of scales (16 bytes, 8 for D 128).
+constexpr int kRawRow = 128, kRawSc = kTile * kRawRow, kRawBytes = kRawSc + kTile * 16;
 constexpr int kUnitCost = 5;                 // see Schedule::ov: 12k cycles at 2.7k a tile (D 512)
 constexpr float kLazy = 15.0f;               // log2 headroom of P below fp16's 65,504
 // TMEM columns: O, S of two tiles (each later its P), Q's first chunks
@@ -82,11 +83,7 @@ struct Cfg {
   static constexpr int NG = D == 128 ? 8 : 4;             // ring groups
   static constexpr int QT = NCH < 4 ? NCH : 4;           // chunks of Q in tensor memory, the first in S's order
   static constexpr int QS = NCH - QT;                    // ... in shared memory
-};
-
-template <int N>
-struct Int {
-  static constexpr int value = N;
+  static constexpr int CB = DO / 2, SB = DO / 16;        // bytes of codes and of scales of a key in a step
 };
 
 // What a block does next: a part of a unit's key list.
@@ -97,7 +94,7 @@ struct Segment {
   int nrows;
   int n_sink, n_fp4, n_win;   // tiles of each sort, in this order
   int key0;                // first entry of the first FP4 tile
-  int key_end;             // entries from here on are not read
+  int key_lo, key_end;     // entries below and from here on count as zeros
   int seq;                 // pool sequence whose table is read (-1: none)
   int slot;                // partial result's place, -1: straight to the output
   int q0, nq;              // queries of the rows
@@ -108,7 +105,7 @@ template <int D>
 struct DenseSmem {
   alignas(1024) uint8_t q[(Cfg<D>::QS > 0 ? Cfg<D>::QS : 1) * kRows * 128];       // chunks of [128 rows x 128 B]
   alignas(1024) uint8_t kv[Cfg<D>::NG][Cfg<D>::GC * kTile * 128];                // groups of chunks [64 keys x 128 B]
-  alignas(16) uint8_t raw[kStages][kRawBytes];
+  alignas(1024) uint8_t raw[kStages][kRawBytes];
   uint64_t raw_full[kStages], raw_empty[kStages];
   uint64_t full[Cfg<D>::NG];
   uint64_t empty[Cfg<D>::NG];
@@ -119,20 +116,28 @@ struct DenseSmem {
   Segment seg[2];                                                                // this one and the next
 };
 
-// Place of 16-byte piece pc of row r in a raw stage: eight lanes that read 4
-// rows x 2 neighbouring pieces meet eight different columns.
+// Place of 16-byte piece pc of row r (of ROW bytes) in a raw stage: the
+// pattern in which a tensor copy with the swizzle of that width writes it.
+// Eight lanes that read a piece of eight neighbouring rows meet eight columns.
+template <int ROW>
 __device__ __forceinline__ uint32_t raw_off(int r, int pc) {
-  return (uint32_t)(r * kRawRow + ((pc ^ ((r & 3) << 1)) << 4));
+  static_assert(ROW == 128 || ROW == 64, "row");
+  return (uint32_t)(r * ROW + ((ROW == 128 ? pc ^ (r & 7) : pc ^ ((r >> 1) & 3)) << 4));
+}
+
+// *p where `live`, else `other`.  Nothing depends on the value until its first
+// use: a select on it (as a conditional expression would be) waits for the load.
+__device__ __forceinline__ int load_if(const int32_t *p, bool live, int other) {
+  int v;
+  asm volatile("{\n.reg .pred q;\nsetp.ne.s32 q, %2, 0;\nmov.b32 %0, %3;\n@q ld.global.nc.b32 %0, [%1];\n}"
+               : "=&r"(v)
+               : "l"(p), "r"((int)live), "r"(other));
+  return v;
 }
 
 // Asynchronous copies to shared memory; `live` false writes zeros instead.
-template <int BYTES>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void *src, bool live) {
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(live ? BYTES : 0), "n"(BYTES)
-                 : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
 // Arrive on `bar` once this thread's copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
@@ -186,6 +191,8 @@ __device__ __forceinline__ long long div64(long long a, long long b) {
 // ------------------------------------------------------------------ schedule of the prefix attention
 
 struct Schedule {
+  int box;                 // entries of a copy: divides the page and the tile
+  int own0;                // first entry of the sequences' own tiles: n_shared rounded down to a box
   int rt_sh, nt_sh;        // row tiles over all rows; key tiles of the prefix
   int rt_own;              // row tiles of a sequence
   int wt;                  // tiles that a window counts for
@@ -195,8 +202,10 @@ struct Schedule {
   int grid;
 };
 
-__host__ __device__ __forceinline__ Schedule make_schedule(const DenseAttnArgs &a, int cs, int grid) {
+inline Schedule make_schedule(const DenseAttnArgs &a, int cs, int grid) {
   Schedule s;
+  s.box = prefix_attn_box(a.pool.page);
+  s.own0 = a.n_shared - a.n_shared % s.box;
   const long long rows = (long long)a.B * a.T_q * a.H;
   s.rt_sh = (int)((rows + kRows - 1) / kRows);
   s.nt_sh = (a.n_shared + kTile - 1) / kTile;
@@ -228,10 +237,10 @@ __device__ __forceinline__ int seq_entries(const DenseAttnArgs &a, int b, int *n
   *n = v < 0 ? 0 : (v > room ? (int)room : v);
   return s;
 }
-__device__ __forceinline__ int own_tiles(const DenseAttnArgs &a, int b) {
+__device__ __forceinline__ int own_tiles(const DenseAttnArgs &a, const Schedule &s, int b) {
   int n;
   seq_entries(a, b, &n);
-  return n > a.n_shared ? (n - a.n_shared + kTile - 1) / kTile : 0;
+  return n > a.n_shared ? (n - s.own0 + kTile - 1) / kTile : 0;
 }
 
 // Workspace: per unit {first slot, slots}, per slot [128] (max, sum), per slot
@@ -270,7 +279,7 @@ __device__ __forceinline__ bool next_prefix_segment(const DenseAttnArgs &a, cons
 #pragma unroll 1
       for (;;) {
         const int bb = b0 + lane;
-        own = bb < a.B ? own_tiles(a, bb) : 0;
+        own = bb < a.B ? own_tiles(a, sc, bb) : 0;
         const long long c = bb < a.B ? sc.rt_own * own_length(sc, own) : 0;
         long long inc = c;
 #pragma unroll
@@ -327,7 +336,8 @@ __device__ __forceinline__ bool next_prefix_segment(const DenseAttnArgs &a, cons
       sg.n_sink = 0;
       sg.n_fp4 = (int)n;
       sg.n_win = win ? 1 : 0;   // counted below
-      sg.key0 = (shared ? 0 : a.n_shared) + (int)tile * kTile;
+      sg.key0 = (shared ? 0 : sc.own0) + (int)tile * kTile;
+      sg.key_lo = shared ? 0 : a.n_shared;
       sg.key_end = shared ? a.n_shared : ents;
       const int u = half * sc.units + unit;
       const int g0 = (int)div64(unit_at + sc.ov, chunk);
@@ -343,12 +353,45 @@ __device__ __forceinline__ bool next_prefix_segment(const DenseAttnArgs &a, cons
   return false;
 }
 
+// Pages of the boxes of a segment's FP4 tiles, tile by tile: lane = box.
+struct BoxPages {
+  const int32_t *row;      // the sequence's page list
+  int e, end;              // first entry of the lane's box in the next tile; the segment's last
+  int idx, off;            // its page's place in the list, its place in the page (advanced without dividing again)
+  int page, adv_p, adv_o;
+  bool mine;
+  __device__ __forceinline__ BoxPages(const Segment &sg, const Schedule &sc, const PagePoolArgs &pool, int lane) {
+    page = pool.page > 0 ? pool.page : 1;
+    row = sg.seq >= 0 ? pool.table + (size_t)sg.seq * pool.max_pages : nullptr;
+    mine = lane * sc.box < kTile;
+    e = sg.key0 + lane * sc.box;
+    end = sg.key_end;
+    idx = e / page;
+    off = e % page;
+    adv_p = kTile / page;
+    adv_o = kTile % page;
+  }
+  // The page of this lane's box (as the list has it; -1 without a list), `none`
+  // where the box holds nothing, `more` says that there is a tile; steps on.
+  __device__ __forceinline__ int next(bool more, int none) {
+    const bool in = more && mine && e < end;
+    const int v = load_if(row + idx, in && row != nullptr, in ? -1 : none);
+    e += kTile;
+    idx += adv_p;
+    off += adv_o;
+    if (off >= page) { off -= page; ++idx; }
+    return v;
+  }
+};
+
 }  // namespace
 
 // MODE 0: prefix attention (paged entries and an optional window), partial
 // results; MODE 1: window with sinks, straight to the output.
 template <int D, int MODE>
-__global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const DenseAttnArgs a, const Schedule sc) {
+__global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_constant__ CUtensorMap codes_map,
+                                                                 const __grid_constant__ CUtensorMap scales_map,
+                                                                 const DenseAttnArgs a, const Schedule sc) {
   using F = Cfg<D>;
   constexpr int DO = F::DO, CS = F::CS, NCH = F::NCH, GC = F::GC, NG = F::NG, QT = F::QT, QS = F::QS;
   constexpr uint32_t kIdS = mma_idesc(kRows, kTile, 0u, 0u);
@@ -449,11 +492,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const DenseAttn
       q_in_place();
       // ---- team t takes the groups whose running number is t modulo 2: the
       // two halves of a tile's channels (D 512), or every other tile.  Lane =
-      // (row, 16-byte piece) so that the eight lanes of a store's phase meet
-      // eight different 16-byte columns of the swizzled rows
+      // (row, 16-byte piece) so that the eight lanes of a load's or a store's
+      // phase meet eight different 16-byte columns of the swizzled rows
       const uint32_t team = warp / kTeam;
-      const int p4 = (lane & 1) | ((lane >> 2) & 2);                                         // piece 0..3 (then 4..7)
-      const int r0 = (warp % kTeam) * 16 + ((lane >> 1) & 3) + ((lane >> 2) & 4);            // keys r0 and r0 + 8
+      const int p4 = lane >> 3;                                // piece 0..3 (then 4..7)
+      const int r0 = (warp % kTeam) * 16 + (lane & 7);         // keys r0 and r0 + 8
       auto hand_over = [&](uint64_t *bar) {   // generic stores -> visible to the tensor core
         fence_proxy_async();
         __syncwarp();
@@ -487,11 +530,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const DenseAttn
           for (int u = 0; u < NU; ++u)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-              rv[u][y] = *reinterpret_cast<const uint4 *>(S.raw[st] + raw_off(r0 + 8 * y, p4 + 4 * u));
-              sb[u][y] = *reinterpret_cast<const uint16_t *>(S.raw[st] + kRawSc + (r0 + 8 * y) * kRawScRow + (p4 + 4 * u) * 2);
+              rv[u][y] = *reinterpret_cast<const uint4 *>(S.raw[st] + raw_off<F::CB>(r0 + 8 * y, p4 + 4 * u));
+              sb[u][y] = *reinterpret_cast<const uint16_t *>(S.raw[st] + kRawSc + (r0 + 8 * y) * F::SB + (p4 + 4 * u) * 2);
             }
           __syncwarp();                                    // this warp's part of the stage is in registers
           if (lane == 0) mbar_arrive(&S.raw_empty[st]);
+          const int k0 = sg.key0 + (it - n_sink) * kTile;
+          if (k0 < sg.key_lo || k0 + kTile > sg.key_end) {   // what the copies brought of other entries: zeros
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const int k = k0 + r0 + 8 * y;
+              if (k >= sg.key_lo && k < sg.key_end) continue;
+#pragma unroll
+              for (int u = 0; u < NU; ++u) {
+                rv[u][y] = make_uint4(0, 0, 0, 0);
+                sb[u][y] = 0;
+              }
+            }
+          }
           ok = all_wait(&S.empty[slot], ph ^ 1u);
           if (!ok) break;
 #pragma unroll
@@ -527,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const DenseAttn
             for (int u = 0; u < 2; ++u)
 #pragma unroll
               for (int y = 0; y < 2; ++y)
-                rv[u][y] = *reinterpret_cast<const uint4 *>(S.raw[st] + raw_off(r0 + 8 * y, p4 + 4 * u));
+                rv[u][y] = *reinterpret_cast<const uint4 *>(S.raw[st] + raw_off<kRawRow>(r0 + 8 * y, p4 + 4 * u));
             __syncwarp();
             if (lane == 0) mbar_arrive(&S.raw_empty[st]);
             if (sub == 0) ok = all_wait(&S.empty[slot], ph ^ 1u);
@@ -607,21 +663,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const DenseAttn
         if (lane == 0) w_ok = wait_or_abort(bar, parity, abort);
         return __shfl_sync(0xffffffffu, w_ok, 0) != 0;
       };
-      const int32_t *trow = sg.seq >= 0 ? a.pool.table + (size_t)sg.seq * a.pool.max_pages : nullptr;
-      // pages of FP4 tile f (lanes 0..4: at most 5 of 16 entries or more): the
-      // bytes of a slot without a page were never read, its keys are hidden
-      auto page_bad = [&](int f) -> bool {
-        const int e0 = sg.key0 + f * kTile;
-        int e1 = e0 + kTile;
-        if (e1 > sg.key_end) e1 = sg.key_end;
-        const int p = e0 / a.pool.page + lane;
-        if (f >= n_fp4 || (long long)p * a.pool.page >= e1) return false;
-        if (!trow) return true;
-        const int pg = __ldg(trow + p);
-        return pg < 0 || pg >= a.pool.n_pages;
-      };
+      // Pages of the next FP4 tile (lane = box of the tile), looked up a tile
+      // ahead and judged when the tile comes: a slot without a page gave zeros,
+      // its keys are hidden.
+      BoxPages pages(sg, sc, a.pool, lane);
       float m_ref = -INFINITY, l = 0.f, vsc = 1.f;
-      bool bad_next = MODE == 0 && page_bad(0);
+      int page_ahead = MODE == 0 ? pages.next(n_fp4 > 0, 0) : 0;
       int wcur = 0;
       bool ok = true;
 #pragma unroll 1
@@ -635,9 +682,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const DenseAttn
           jb = (snk < sg.key_end ? snk : sg.key_end) - it * kTile;
           ksc = a.s_sink;
         } else if (it < n_sink + n_fp4) {
-          jb = vis - (sg.key0 + (it - n_sink) * kTile);
-          badp = __ballot_sync(0xffffffffu, bad_next);
-          bad_next = page_bad(it - n_sink + 1);
+          const int k0 = sg.key0 + (it - n_sink) * kTile;
+          ja = sg.key_lo - k0;
+          jb = vis - k0;
+          badp = __ballot_sync(0xffffffffu, (uint32_t)page_ahead >= (uint32_t)a.pool.n_pages);
+          page_ahead = pages.next(it + 1 < n_sink + n_fp4, 0);
         } else {
           int s = 0, e = 0;
           next_window(sg, a.window, wcur, lane, &s, &e);
@@ -665,10 +714,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const DenseAttn
           uint64_t seen = hi > lo ? (~0ull >> (kTile - (hi - lo))) << lo : 0ull;
           if (badp) {   // rare
             if (lane == 0) flag(a.status, CSA2_DEV_INDEX_RANGE);
-            const int e0 = sg.key0 + (it - n_sink) * kTile, p0 = e0 / a.pool.page;
 #pragma unroll 1
             for (int j = 0; j < kTile; ++j)
-              if ((badp >> ((e0 + j) / a.pool.page - p0)) & 1u) seen &= ~(1ull << j);
+              if ((badp >> (j / sc.box)) & 1u) seen &= ~(1ull << j);
           }
           const uint32_t s_lo = (uint32_t)seen, s_hi = (uint32_t)(seen >> 32);
 #pragma unroll
@@ -802,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const DenseAttn
       long long th = 0, chunk = 1, x, x_end;
       if (MODE == 0) {
         long long sum = 0;
-        for (int b = lane; b < a.B; b += 32) sum += own_length(sc, own_tiles(a, b));
+        for (int b = lane; b < a.B; b += 32) sum += own_length(sc, own_tiles(a, sc, b));
 #pragma unroll 1
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         th = sc.rt_sh * shared_length(sc) + sc.rt_own * sum;
@@ -956,104 +1004,95 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const DenseAttn
         }
         __syncwarp();
       } else if (warp == kLoadWarp) {
-        // ---- the raw steps: lane = key r of the tile for its address; a copy's
-        // lanes lie along the rows (a row's 256 bytes by 16 lanes)
-        const int page = a.pool.page > 0 ? a.pool.page : 1;
-        const int32_t *trow = sg.seq >= 0 ? a.pool.table + (size_t)sg.seq * a.pool.max_pages : nullptr;
-        // FP4: places of the lane's two keys in the page list, advanced tile by
-        // tile; their pages are looked up a tile ahead
-        const int adv_p = kTile / page, adv_o = kTile % page;
-        int e_cur = sg.key0 + lane, left = n_fp4;
-        int p_idx[2] = {e_cur / page, (e_cur + 32) / page}, p_off[2] = {e_cur % page, (e_cur + 32) % page}, pg_next[2];
-        auto page_of = [&](int y) -> int {
-          return left > 0 && trow && e_cur + 32 * y < sg.key_end ? __ldg(trow + p_idx[y]) : -1;
-        };
-        pg_next[0] = page_of(0);
-        pg_next[1] = page_of(1);
+        // ---- the raw steps.  FP4: the page's boxes by tensor copies, lane =
+        // box (codes, then scales; rows behind the pool are filled with zeros:
+        // that is where boxes without a page point).  FP8: rows by
+        // asynchronous copies, whose lanes lie along the rows
+        BoxPages pages(sg, sc, a.pool, lane);
+        int off = pages.off, page_ahead = MODE == 0 ? pages.next(n_fp4 > 0, -1) : 0;
+        const int nowhere = a.pool.n_pages * a.pool.page;
         int wcur = 0;
         bool ok = true;
         auto acquire = [&](uint32_t st) {
           return __all_sync(0xffffffffu, wait_or_abort(&S.raw_empty[st], ((scount / kStages) & 1u) ^ 1u, abort)) != 0;
         };
-        // 32 rows from row0 on of stage st: LPR lanes of 16 bytes per row; p: the
-        // address of this lane's key, nullptr = zeros
-        auto copy_rows = [&](uint32_t st, int row0, const uint8_t *p, auto lpr) {
-          constexpr int LPR = decltype(lpr)::value, RPI = 32 / LPR;
-          const unsigned long long mine = reinterpret_cast<unsigned long long>(p);
-          const uint8_t *any = a.pool.codes ? a.pool.codes : (a.swa_rows ? a.swa_rows : a.sink_rows);
-          const uint32_t dst = smem_u32(S.raw[st]);
+        auto share_rows = [&](int y, int mine, int *rows) {   // rows[8 y + i]: row of key 32 y + 4 i + lane / 8
 #pragma unroll
-          for (int i = 0; i < LPR; ++i) {
-            const int row = i * RPI + lane / LPR, pc = lane % LPR;
-            const uint8_t *src = reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, mine, row));
-            cp_async<16>(dst + raw_off(row0 + row, pc), src ? src + pc * 16 : any, src != nullptr);
-          }
+          for (int i = 0; i < 8; ++i) rows[y * 8 + i] = __shfl_sync(0xffffffffu, mine, i * 4 + lane / 8);
         };
+        if (MODE == 0) fence_proxy_async();   // stages that the last segment's window wrote
 #pragma unroll 1
         for (int it = 0; it < n_tiles && ok; ++it) {
-          if (it >= n_sink && it < n_sink + n_fp4) {
-            size_t er[2];
-            bool have[2];
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              have[y] = pg_next[y] >= 0 && pg_next[y] < a.pool.n_pages;
-              er[y] = have[y] ? (size_t)pg_next[y] * page + p_off[y] : 0;
-              p_idx[y] += adv_p;
-              p_off[y] += adv_o;
-              if (p_off[y] >= page) { p_off[y] -= page; ++p_idx[y]; }
-            }
-            --left;
-            e_cur += kTile;
-            pg_next[0] = page_of(0);
-            pg_next[1] = page_of(1);
+          if (MODE == 0 && it < n_fp4) {
+            int er = (uint32_t)page_ahead < (uint32_t)a.pool.n_pages ? page_ahead * a.pool.page + off : nowhere;
+            off = pages.off;
+            page_ahead = pages.next(it + 1 < n_fp4, -1);
 #pragma unroll 1
             for (int g = 0; g < CS; ++g) {
               const uint32_t st = scount % kStages;
               ok = acquire(st);
               if (!ok) break;
               const int c0 = q_chunk(g * GC, half);
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                copy_rows(st, 32 * y, have[y] ? a.pool.codes + er[y] * (D / 2) + c0 * 32 : nullptr, Int<GC * 2>{});
-                constexpr int SB = GC * 4;   // scale bytes of a key in a step
-                cp_async<SB>(smem_u32(S.raw[st]) + kRawSc + (32 * y + lane) * kRawScRow,
-                             a.pool.scales + er[y] * (D / 16) + c0 * 4, have[y]);
+              if (lane == 0) {
+                mbar_arrive_expect_tx(&S.raw_full[st], kTile * (F::CB + F::SB));
+                mbar_arrive_n(&S.raw_full[st], 31);
               }
-              cp_async_arrive(&S.raw_full[st]);
+              __syncwarp();
+              if (lane * sc.box < kTile) {
+                uint8_t *raw = S.raw[st];
+                tma_load_2d(raw + lane * sc.box * F::CB, &codes_map, c0 * 32, er, &S.raw_full[st]);
+                if (D == 128)   // two keys' scales make a row of the map
+                  tma_load_2d(raw + kRawSc + lane * sc.box * F::SB, &scales_map, 0, er >> 1, &S.raw_full[st]);
+                else
+                  tma_load_2d(raw + kRawSc + lane * sc.box * F::SB, &scales_map, c0 * 4, er, &S.raw_full[st]);
+              }
               ++scount;
             }
           } else {
-            const uint8_t *row[2] = {nullptr, nullptr};
+            const uint8_t *base;                   // the rows' sequence
+            int row[2] = {-1, -1};
             if (it < n_sink) {
+              base = a.sink_rows + (size_t)sg.b * a.sink_cap * D;
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
                 const int key = it * kTile + 32 * y + lane;
-                if (key < sg.key_end) row[y] = a.sink_rows + ((size_t)sg.b * a.sink_cap + key) * D;
+                if (key < sg.key_end) row[y] = key;
               }
             } else {
+              base = a.swa_rows + (size_t)sg.b * a.W_cap * D;
               int s = 0, e = 0;
               next_window(sg, a.window, wcur, lane, &s, &e);
               wcur = e;
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
                 const int tok = s + 32 * y + lane;
-                if (tok < e) row[y] = a.swa_rows + ((size_t)sg.b * a.W_cap + tok % a.W_cap) * D;
+                if (tok < e) row[y] = tok % a.W_cap;
               }
             }
+            int rows[16];
+            share_rows(0, row[0], rows);
+            share_rows(1, row[1], rows);
 #pragma unroll 1
             for (int k = 0; k < NCH; k += 2) {   // two chunks a step, in S's order
               const uint32_t st = scount % kStages;
               ok = acquire(st);
               if (!ok) break;
+              const uint32_t dst = smem_u32(S.raw[st]);
+              const uint8_t *src = base + q_chunk(k, half) * 64 + (lane & 7) * 16;
 #pragma unroll
-              for (int y = 0; y < 2; ++y)
-                copy_rows(st, 32 * y, row[y] ? row[y] + q_chunk(k, half) * 64 : nullptr, Int<8>{});
+              for (int i = 0; i < 16; ++i)
+                cp_async16(dst + raw_off<kRawRow>(4 * i + lane / 8, lane & 7), src + (size_t)(rows[i] < 0 ? 0 : rows[i]) * D,
+                           rows[i] >= 0);
               cp_async_arrive(&S.raw_full[st]);
               ++scount;
             }
           }
         }
-        cp_async_wait_all();   // none in flight when the segment (or, after a wait that gave up, the block) ends
+        // none in flight when the segment (or, after a wait that gave up, the block) ends
+        cp_async_wait_all();
+        for (uint32_t u = scount < kStages ? 0 : scount - kStages; u < scount; ++u)
+          mbar_wait_bounded(&S.raw_full[u % kStages], (u / kStages) & 1u, kWaitLimit);
+        __syncwarp();
       }
       tcount += n_tiles;
       dead = end_segment();
@@ -1106,7 +1145,7 @@ __global__ void __launch_bounds__(kRows * kMergeShares) attn_dense_merge_kernel(
   const float4 *po = reinterpret_cast<const float4 *>(ws + w.off_o);
   int2 sh = make_int2(0, 0), ow = make_int2(0, 0);   // (first slot, slots) of the prefix and of the row's own keys
   if (live && sc.nt_sh > 0) sh = __ldcg(desc + blockIdx.x);
-  if (live && own_tiles(a, b) + sc.wt > 0) ow = __ldcg(desc + sc.rt_sh + b * sc.rt_own + orow / kRows);
+  if (live && own_tiles(a, sc, b) + sc.wt > 0) ow = __ldcg(desc + sc.rt_sh + b * sc.rt_own + orow / kRows);
   const int parts = sh.y + ow.y;
   auto place = [&](int s) -> size_t {   // part s: slot * 128 + row of the slot
     return s < sh.y ? (size_t)(sh.x + s) * kRows + row : (size_t)(ow.x + s - sh.y) * kRows + orow % kRows;
@@ -1178,19 +1217,20 @@ long long prefix_units(int B, int T_q, int H, int D) {
 }
 
 template <int D, int MODE>
-cudaError_t launch_dense(const DenseAttnArgs &a, const Schedule &sc, cudaStream_t s) {
+cudaError_t launch_dense(const CUtensorMap &codes, const CUtensorMap &scales, const DenseAttnArgs &a, const Schedule &sc,
+                         cudaStream_t s) {
   const size_t smem = sizeof(DenseSmem<D>) + 1024;
   static_assert(sizeof(DenseSmem<D>) + 1024 <= 232448, "shared memory");
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t e = allow_smem_once(attn_dense_kernel<D, MODE>, smem, &allowed);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_dense_kernel<D, MODE>, dim3(sc.grid), dim3(kThreads), smem, s, dim3(1, 1, 1), a, sc);
+  return launch_pdl(attn_dense_kernel<D, MODE>, dim3(sc.grid), dim3(kThreads), smem, s, dim3(1, 1, 1), codes, scales, a, sc);
 }
 
 template <int D>
-cudaError_t launch_prefix_t(const DenseAttnArgs &a, int sms, cudaStream_t s) {
+cudaError_t launch_prefix_t(const CUtensorMap &codes, const CUtensorMap &scales, const DenseAttnArgs &a, int sms, cudaStream_t s) {
   const Schedule sc = make_schedule(a, Cfg<D>::CS, sms);
-  cudaError_t e = launch_dense<D, 0>(a, sc, s);
+  cudaError_t e = launch_dense<D, 0>(codes, scales, a, sc, s);
   if (e != cudaSuccess) return e;
   return launch_pdl(attn_dense_merge_kernel<D>, dim3(sc.rt_sh, D / kMergeCh), dim3(kRows * kMergeShares), 0, s, dim3(1, 1, 1), a, sc);
 }
@@ -1200,7 +1240,8 @@ cudaError_t launch_window_t(const DenseAttnArgs &a, int sms, cudaStream_t s) {
   Schedule sc = make_schedule(a, Cfg<D>::CS, sms);
   const long long units = (long long)a.B * sc.rt_own * Cfg<D>::CS;
   if (units < sc.grid) sc.grid = (int)units;
-  return launch_dense<D, 1>(a, sc, s);
+  const CUtensorMap none{};   // no entries
+  return launch_dense<D, 1>(none, none, a, sc, s);
 }
 
 }  // namespace
@@ -1208,11 +1249,12 @@ cudaError_t launch_window_t(const DenseAttnArgs &a, int sms, cudaStream_t s) {
 size_t prefix_attn_workspace_bytes(int B, int T_q, int H, int D, int sms) {
   return dense_ws(prefix_units(B, T_q, H, D), sms, D < 256 ? D : 256).bytes;
 }
-cudaError_t launch_prefix_attn(const DenseAttnArgs &a, int sms, cudaStream_t s) {
+cudaError_t launch_prefix_attn(const CUtensorMap &codes, const CUtensorMap &scales, const DenseAttnArgs &a, int sms,
+                               cudaStream_t s) {
   switch (a.D) {
-    case 128: return launch_prefix_t<128>(a, sms, s);
-    case 256: return launch_prefix_t<256>(a, sms, s);
-    default: return launch_prefix_t<512>(a, sms, s);
+    case 128: return launch_prefix_t<128>(codes, scales, a, sms, s);
+    case 256: return launch_prefix_t<256>(codes, scales, a, sms, s);
+    default: return launch_prefix_t<512>(codes, scales, a, sms, s);
   }
 }
 size_t window_attn_workspace_bytes(int, int, int, int, int, int, int) { return 0; }
