@@ -69,7 +69,7 @@ constexpr int kStages = 3;                   // raw steps in flight or in use
 // A stage: 64 rows of 128 bytes (codes, 64 bytes for D 128, or FP8 values),
 // then 64 rows of scales (16 bytes, 8 for D 128).
 constexpr int kRawRow = 128, kRawSc = kTile * kRawRow, kRawBytes = kRawSc + kTile * 16;
-constexpr int kUnitCost = 5;                 // see Schedule::ov: 12k cycles at 2.7k a tile (D 512)
+constexpr int kUnitCost = 8;                 // see Schedule::ov: 12k cycles at 2.7k a tile (D 512)
 constexpr float kLazy = 15.0f;               // log2 headroom of P below fp16's 65,504
 // TMEM columns: O, S of two tiles (each later its P), Q's first chunks
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 384, kTmemCols = 512;
@@ -109,6 +109,7 @@ struct DenseSmem {
   uint64_t raw_full[kStages], raw_empty[kStages];
   uint64_t full[Cfg<D>::NG];
   uint64_t empty[Cfg<D>::NG];
+  uint64_t q_full;                                                               // a segment's Q has landed
   uint64_t s_full[2], p_full[2], pv_done[2], fin;                                // of a tile's buffer
   uint32_t tmem_base;
   int abort;
@@ -389,7 +390,8 @@ struct BoxPages {
 // MODE 0: prefix attention (paged entries and an optional window), partial
 // results; MODE 1: window with sinks, straight to the output.
 template <int D, int MODE>
-__global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_constant__ CUtensorMap codes_map,
+__global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_constant__ CUtensorMap q_map,
+                                                                 const __grid_constant__ CUtensorMap codes_map,
                                                                  const __grid_constant__ CUtensorMap scales_map,
                                                                  const DenseAttnArgs a, const Schedule sc) {
   using F = Cfg<D>;
@@ -416,6 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
       mbar_init(&S.p_full[u], 4);
       mbar_init(&S.pv_done[u], 1);
     }
+    mbar_init(&S.q_full, 1);
     mbar_init(&S.fin, 2);
     S.abort = 0;
     fence_barrier_init();
@@ -454,6 +457,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
     const __half2 hv = __floats2half2_rn(bf16_to_f32(w & 0xFFFFu) * qsign, bf16_to_f32(w >> 16) * qsign);
     return *reinterpret_cast<const uint32_t *>(&hv);
   };
+  auto all_wait = [&](uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort)) != 0;
+  };
   uint32_t gcount = 0, tcount = 0;   // ring groups and tiles so far (each role advances them alike)
   uint32_t scount = 0;               // raw steps so far (load and dequantise)
 
@@ -462,29 +468,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFetch));
     while (begin_segment()) {
       const Segment &sg = S.seg[seg_i & 1u];
+      // (what the tile loop needs in registers: beside the S product a load from
+      // shared memory takes 320 cycles instead of 43)
       const int n_sink = sg.n_sink, n_fp4 = sg.n_fp4, n_tiles = n_sink + n_fp4 + sg.n_win;
-      const int half = sg.half;
-      // ---- Q's chunks of shared memory, rows behind the last one zero
+      const int key0 = sg.key0, key_lo = sg.key_lo, key_end = sg.key_end;
+      // ---- Q's chunks of shared memory: bf16 -> fp16 in place
+      bool ok = all_wait(&S.q_full, seg_i & 1u);
       if constexpr (QS > 0) {
-        const uint16_t *qrow = a.q + (size_t)sg.row0 * D;
-        const int nrows = sg.nrows;
-        constexpr int NP = kRows * QS * 8;   // 16-byte pieces
-#pragma unroll 1
-        for (int i0 = tid; i0 < NP; i0 += kDq * 8) {
-          uint4 v[8];
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const int i = i0 + u * kDq, r = i / (QS * 8), pc = i % (QS * 8);
-            v[u] = (i < NP && r < nrows)
-                       ? __ldg(reinterpret_cast<const uint4 *>(qrow + (size_t)r * D + q_chunk(QT + (pc >> 3), half) * 64) + (pc & 7))
-                       : make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const int i = i0 + u * kDq, r = i / (QS * 8), pc = i % (QS * 8);
-            if (i < NP)
-              *reinterpret_cast<uint4 *>(S.q + sw_off(r, pc, kRows)) =
-                  make_uint4(to_f16x2(v[u].x), to_f16x2(v[u].y), to_f16x2(v[u].z), to_f16x2(v[u].w));
+        if (ok) {
+#pragma unroll 4
+          for (int i = tid; i < kRows * QS * 8; i += kDq) {
+            uint4 *p = reinterpret_cast<uint4 *>(S.q) + i;
+            const uint4 v = *p;
+            *p = make_uint4(to_f16x2(v.x), to_f16x2(v.y), to_f16x2(v.z), to_f16x2(v.w));
           }
         }
         fence_proxy_async();
@@ -502,11 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
       };
-      auto all_wait = [&](uint64_t *bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort)) != 0;
-      };
       constexpr int FP8_S = GC / 2;                        // steps of a group of FP8 rows
-      bool ok = true;
 #pragma unroll 1
       for (int it = 0; it < n_tiles && ok; ++it) {
         const bool fp4 = it >= n_sink && it < n_sink + n_fp4;
@@ -535,12 +527,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
             }
           __syncwarp();                                    // this warp's part of the stage is in registers
           if (lane == 0) mbar_arrive(&S.raw_empty[st]);
-          const int k0 = sg.key0 + (it - n_sink) * kTile;
-          if (k0 < sg.key_lo || k0 + kTile > sg.key_end) {   // what the copies brought of other entries: zeros
+          const int k0 = key0 + (it - n_sink) * kTile;
+          if (k0 < key_lo || k0 + kTile > key_end) {   // what the copies brought of other entries: zeros
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
               const int k = k0 + r0 + 8 * y;
-              if (k >= sg.key_lo && k < sg.key_end) continue;
+              if (k >= key_lo && k < key_end) continue;
 #pragma unroll
               for (int u = 0; u < NU; ++u) {
                 rv[u][y] = make_uint4(0, 0, 0, 0);
@@ -618,25 +610,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
       const Segment &sg = S.seg[seg_i & 1u];
       const int n_sink = sg.n_sink, n_fp4 = sg.n_fp4, n_tiles = n_sink + n_fp4 + sg.n_win;
       const int half = sg.half;
+      const int key0 = sg.key0, key_lo = sg.key_lo, key_end = sg.key_end;
       const int q = warp & 3, row = 32 * q + lane;
       const uint32_t lrow = tmem + ((uint32_t)(32 * q) << 16);
       const int frow = sg.row0 + row;
       const bool live = row < sg.nrows;
-      // ---- Q's first chunks: this thread's row into its tensor-memory lane
-      {
-        const uint4 *qp = reinterpret_cast<const uint4 *>(a.q + (size_t)frow * D);
-        uint4 v[QT][8];
-#pragma unroll
-        for (int k = 0; k < QT; ++k)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[k][i] = live ? __ldg(qp + q_chunk(k, half) * 8 + i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int k = 0; k < QT; ++k) {
+      // ---- Q's first chunks, which landed in the ring (no group is in use
+      // yet): this thread's row into its tensor-memory lane.  A rolled loop: at
+      // a kernel's start the instructions come from far
+      bool ok = all_wait(&S.q_full, seg_i & 1u);
+      if (ok) {
+        const uint8_t *qs = S.kv[0] + row * 128;
+#pragma unroll 1
+        for (int k = 0; k < QT; ++k, qs += kRows * 128) {
           uint32_t h[32];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            h[4 * i] = to_f16x2(v[k][i].x); h[4 * i + 1] = to_f16x2(v[k][i].y);
-            h[4 * i + 2] = to_f16x2(v[k][i].z); h[4 * i + 3] = to_f16x2(v[k][i].w);
+            const uint4 v = *reinterpret_cast<const uint4 *>(qs + ((i ^ (row & 7)) << 4));
+            h[4 * i] = to_f16x2(v.x); h[4 * i + 1] = to_f16x2(v.y);
+            h[4 * i + 2] = to_f16x2(v.z); h[4 * i + 3] = to_f16x2(v.w);
           }
           tmem_st_x32(lrow + kColQ + 32 * k, h);
         }
@@ -653,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
         if (seq_entries(a, b, &n) < 0) flag(a.status, CSA2_DEV_BAD_SEQUENCE);
         const int v = (t + 1) / a.pool.m;
         vis = n < v ? n : v;
-        if (vis > sg.key_end) vis = sg.key_end;
+        if (vis > key_end) vis = key_end;
       }
       int wlo = t - a.window + 1;
       if (wlo < 0) wlo = 0;
@@ -670,20 +662,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
       float m_ref = -INFINITY, l = 0.f, vsc = 1.f;
       int page_ahead = MODE == 0 ? pages.next(n_fp4 > 0, 0) : 0;
       int wcur = 0;
-      bool ok = true;
 #pragma unroll 1
-      for (int it = 0; it < n_tiles; ++it) {
+      for (int it = 0; it < n_tiles && ok; ++it) {
         const uint32_t tc = tcount + it;
         // the keys of this tile that this row sees: [ja, jb)
         int ja = 0, jb;
         float ksc = 1.f;
         uint32_t badp = 0;
         if (it < n_sink) {
-          jb = (snk < sg.key_end ? snk : sg.key_end) - it * kTile;
+          jb = (snk < key_end ? snk : key_end) - it * kTile;
           ksc = a.s_sink;
         } else if (it < n_sink + n_fp4) {
-          const int k0 = sg.key0 + (it - n_sink) * kTile;
-          ja = sg.key_lo - k0;
+          const int k0 = key0 + (it - n_sink) * kTile;
+          ja = key_lo - k0;
           jb = vis - k0;
           badp = __ballot_sync(0xffffffffu, (uint32_t)page_ahead >= (uint32_t)a.pool.n_pages);
           page_ahead = pages.next(it + 1 < n_sink + n_fp4, 0);
@@ -874,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
             sg.half = half; sg.b = b;
             sg.row0 = b * rows + rt * kRows;
             sg.nrows = rows - rt * kRows < kRows ? rows - rt * kRows : kRows;
-            sg.n_fp4 = 0; sg.key0 = 0; sg.key_end = 0; sg.seq = -1; sg.slot = -1;
+            sg.n_fp4 = 0; sg.key0 = 0; sg.key_lo = 0; sg.key_end = 0; sg.seq = -1; sg.slot = -1;
             sg.n_sink = 0;
             sg.n_win = 1;
           }
@@ -1004,6 +995,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
         }
         __syncwarp();
       } else if (warp == kLoadWarp) {
+        // ---- Q by tensor copies, in S's order of the chunks: the first into the
+        // ring, the rest into their own place (rows that are not the unit's
+        // are not seen by anything that leaves the block)
+        if (lane == 0) {
+          fence_proxy_async();
+          mbar_arrive_expect_tx(&S.q_full, NCH * kRows * 128);
+#pragma unroll 1
+          for (int k = 0; k < NCH; ++k)
+            tma_load_2d(k < QT ? S.kv[0] + k * (kRows * 128) : S.q + (k - QT) * (kRows * 128), &q_map, q_chunk(k, half) * 64,
+                        sg.row0, &S.q_full);
+        }
+        __syncwarp();
         // ---- the raw steps.  FP4: the page's boxes by tensor copies, lane =
         // box (codes, then scales; rows behind the pool are filled with zeros:
         // that is where boxes without a page point).  FP8: rows by
@@ -1090,6 +1093,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
         }
         // none in flight when the segment (or, after a wait that gave up, the block) ends
         cp_async_wait_all();
+        mbar_wait_bounded(&S.q_full, seg_i & 1u, kWaitLimit);
         for (uint32_t u = scount < kStages ? 0 : scount - kStages; u < scount; ++u)
           mbar_wait_bounded(&S.raw_full[u % kStages], (u / kStages) & 1u, kWaitLimit);
         __syncwarp();
@@ -1217,31 +1221,32 @@ long long prefix_units(int B, int T_q, int H, int D) {
 }
 
 template <int D, int MODE>
-cudaError_t launch_dense(const CUtensorMap &codes, const CUtensorMap &scales, const DenseAttnArgs &a, const Schedule &sc,
+cudaError_t launch_dense(const CUtensorMap &q, const CUtensorMap &codes, const CUtensorMap &scales, const DenseAttnArgs &a, const Schedule &sc,
                          cudaStream_t s) {
   const size_t smem = sizeof(DenseSmem<D>) + 1024;
   static_assert(sizeof(DenseSmem<D>) + 1024 <= 232448, "shared memory");
+  static_assert(Cfg<D>::QT * kRows <= Cfg<D>::NG * Cfg<D>::GC * kTile, "Q's staging in the ring");
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t e = allow_smem_once(attn_dense_kernel<D, MODE>, smem, &allowed);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_dense_kernel<D, MODE>, dim3(sc.grid), dim3(kThreads), smem, s, dim3(1, 1, 1), codes, scales, a, sc);
+  return launch_pdl(attn_dense_kernel<D, MODE>, dim3(sc.grid), dim3(kThreads), smem, s, dim3(1, 1, 1), q, codes, scales, a, sc);
 }
 
 template <int D>
-cudaError_t launch_prefix_t(const CUtensorMap &codes, const CUtensorMap &scales, const DenseAttnArgs &a, int sms, cudaStream_t s) {
+cudaError_t launch_prefix_t(const CUtensorMap &q, const CUtensorMap &codes, const CUtensorMap &scales, const DenseAttnArgs &a, int sms, cudaStream_t s) {
   const Schedule sc = make_schedule(a, Cfg<D>::CS, sms);
-  cudaError_t e = launch_dense<D, 0>(codes, scales, a, sc, s);
+  cudaError_t e = launch_dense<D, 0>(q, codes, scales, a, sc, s);
   if (e != cudaSuccess) return e;
   return launch_pdl(attn_dense_merge_kernel<D>, dim3(sc.rt_sh, D / kMergeCh), dim3(kRows * kMergeShares), 0, s, dim3(1, 1, 1), a, sc);
 }
 
 template <int D>
-cudaError_t launch_window_t(const DenseAttnArgs &a, int sms, cudaStream_t s) {
+cudaError_t launch_window_t(const CUtensorMap &q, const DenseAttnArgs &a, int sms, cudaStream_t s) {
   Schedule sc = make_schedule(a, Cfg<D>::CS, sms);
   const long long units = (long long)a.B * sc.rt_own * Cfg<D>::CS;
   if (units < sc.grid) sc.grid = (int)units;
   const CUtensorMap none{};   // no entries
-  return launch_dense<D, 1>(none, none, a, sc, s);
+  return launch_dense<D, 1>(q, none, none, a, sc, s);
 }
 
 }  // namespace
@@ -1249,20 +1254,20 @@ cudaError_t launch_window_t(const DenseAttnArgs &a, int sms, cudaStream_t s) {
 size_t prefix_attn_workspace_bytes(int B, int T_q, int H, int D, int sms) {
   return dense_ws(prefix_units(B, T_q, H, D), sms, D < 256 ? D : 256).bytes;
 }
-cudaError_t launch_prefix_attn(const CUtensorMap &codes, const CUtensorMap &scales, const DenseAttnArgs &a, int sms,
-                               cudaStream_t s) {
+cudaError_t launch_prefix_attn(const CUtensorMap &q, const CUtensorMap &codes, const CUtensorMap &scales,
+                               const DenseAttnArgs &a, int sms, cudaStream_t s) {
   switch (a.D) {
-    case 128: return launch_prefix_t<128>(codes, scales, a, sms, s);
-    case 256: return launch_prefix_t<256>(codes, scales, a, sms, s);
-    default: return launch_prefix_t<512>(codes, scales, a, sms, s);
+    case 128: return launch_prefix_t<128>(q, codes, scales, a, sms, s);
+    case 256: return launch_prefix_t<256>(q, codes, scales, a, sms, s);
+    default: return launch_prefix_t<512>(q, codes, scales, a, sms, s);
   }
 }
 size_t window_attn_workspace_bytes(int, int, int, int, int, int, int) { return 0; }
-cudaError_t launch_window_attn(const DenseAttnArgs &a, int sms, cudaStream_t s) {
+cudaError_t launch_window_attn(const CUtensorMap &q, const DenseAttnArgs &a, int sms, cudaStream_t s) {
   switch (a.D) {
-    case 128: return launch_window_t<128>(a, sms, s);
-    case 256: return launch_window_t<256>(a, sms, s);
-    default: return launch_window_t<512>(a, sms, s);
+    case 128: return launch_window_t<128>(q, a, sms, s);
+    case 256: return launch_window_t<256>(q, a, sms, s);
+    default: return launch_window_t<512>(q, a, sms, s);
   }
 }
 

@@ -597,6 +597,12 @@ def test_prompt_forked_into_samples_that_decode():
             values[b].append(fp4_values(tail.codes[b, :1], tail.scales[b, :1]))
             check(out[b, 0], *attend64(q[b, 0].double(), torch.cat(values[b]), scale), f"step {step} b {b}")
     C.csa2_pages_fork(pool, i32([-1]), i32([1]))
+    # (an ended sample has no keys, which moves the cuts of the work: the sums
+    # of the others are joined in another order than before)
+    C.csa2_prefix_attn_decode(pool, seq, n0, None, q, pos, scale, out)
+    for b in range(S):
+        if int(seq[b]) != 1:
+            check(out[b, 0], *attend64(q[b, 0].double(), torch.cat(values[b]), scale), f"ended, b {b}")
     live = torch.zeros(1, dtype=torch.int32, device="cuda")
     C.csa2_pages_compact(pool, live)
     assert int(live) == int((pool.refs > 0).sum())
