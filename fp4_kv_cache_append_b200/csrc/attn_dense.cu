@@ -1124,14 +1124,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
 
 // Joins the parts of every row: out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.
 // Block: a row tile of 128 flattened rows x 8 channels; thread = (row, share of
-// the parts), so that a row's parts are in flight together; the parts' planes
-// are [channel / 4][row], so every load is coalesced.
-constexpr int kMergeShares = 4, kMergeCh = 8;
+// the parts).  One pass with a running maximum, kMergeBatch parts in flight per
+// thread; the parts' planes are [channel / 4][row], so every load is coalesced.
+constexpr int kMergeShares = 4, kMergeCh = 8, kMergeBatch = 2;
 template <int D>
-__global__ void __launch_bounds__(kRows * kMergeShares) attn_dense_merge_kernel(const DenseAttnArgs a, const Schedule sc) {
+__global__ void __launch_bounds__(kRows * kMergeShares, 2) attn_dense_merge_kernel(const DenseAttnArgs a, const Schedule sc) {
   using F = Cfg<D>;
   constexpr int DO = F::DO;
-  __shared__ float red[kMergeShares][kRows];
+  __shared__ float2 red[kMergeShares][kRows];   // (maximum, sum) of a share
   __shared__ float4 racc[kMergeShares - 1][kMergeCh / 4][kRows];
   const int row = threadIdx.x % kRows, share = threadIdx.x / kRows;
   pdl_launch_dependents();
@@ -1154,55 +1154,78 @@ __global__ void __launch_bounds__(kRows * kMergeShares) attn_dense_merge_kernel(
   auto place = [&](int s) -> size_t {   // part s: slot * 128 + row of the slot
     return s < sh.y ? (size_t)(sh.x + s) * kRows + row : (size_t)(ow.x + s - sh.y) * kRows + orow % kRows;
   };
-  float M = -INFINITY;
-#pragma unroll 4
-  for (int s = share; s < parts; s += kMergeShares) M = fmaxf(M, __ldcg(&ml[place(s)]).x);
-  red[share][row] = M;
-  __syncthreads();
-#pragma unroll
-  for (int u = 0; u < kMergeShares; ++u) M = fmaxf(M, red[u][row]);
-  const float Mu = M == -INFINITY ? 0.f : M;
+  float M = -INFINITY, L = 0.f;
   float4 acc[kMergeCh / 4];
 #pragma unroll
   for (int j = 0; j < kMergeCh / 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-  float L = 0.f;
-#pragma unroll 4
-  for (int s = share; s < parts; s += kMergeShares) {
-    const size_t at = place(s), slot = at / kRows, r = at % kRows;
-    const float2 v = __ldcg(&ml[at]);
-    const float4 *p = po + (slot * (DO / 4) + c0 / 4) * kRows + r;
-    float4 o[kMergeCh / 4];
+#pragma unroll 1
+  for (int s0 = share; s0 < parts; s0 += kMergeShares * kMergeBatch) {
+    float2 v[kMergeBatch];
+    float4 o[kMergeBatch][kMergeCh / 4];
 #pragma unroll
-    for (int j = 0; j < kMergeCh / 4; ++j) o[j] = __ldcg(p + (size_t)j * kRows);
-    const float f = exp2f(v.x - Mu);
-    L = fmaf(f, v.y, L);
+    for (int u = 0; u < kMergeBatch; ++u) {
+      const int s = s0 + u * kMergeShares;
+      v[u] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-    for (int j = 0; j < kMergeCh / 4; ++j) {
-      acc[j].x = fmaf(f, o[j].x, acc[j].x);
-      acc[j].y = fmaf(f, o[j].y, acc[j].y);
-      acc[j].z = fmaf(f, o[j].z, acc[j].z);
-      acc[j].w = fmaf(f, o[j].w, acc[j].w);
+      for (int j = 0; j < kMergeCh / 4; ++j) o[u][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (s < parts) {
+        const size_t at = place(s);
+        const float4 *p = po + (at / kRows * (DO / 4) + c0 / 4) * kRows + at % kRows;
+        v[u] = __ldcg(&ml[at]);
+#pragma unroll
+        for (int j = 0; j < kMergeCh / 4; ++j) o[u][j] = __ldcg(p + (size_t)j * kRows);
+      }
+    }
+    float Mn = M;
+#pragma unroll
+    for (int u = 0; u < kMergeBatch; ++u) Mn = fmaxf(Mn, v[u].x);
+    const float Mu = Mn == -INFINITY ? 0.f : Mn;
+    const float f0 = exp2f(M - Mu);
+    M = Mn;
+    L *= f0;
+#pragma unroll
+    for (int j = 0; j < kMergeCh / 4; ++j) { acc[j].x *= f0; acc[j].y *= f0; acc[j].z *= f0; acc[j].w *= f0; }
+#pragma unroll
+    for (int u = 0; u < kMergeBatch; ++u) {
+      const float f = exp2f(v[u].x - Mu);
+      L = fmaf(f, v[u].y, L);
+#pragma unroll
+      for (int j = 0; j < kMergeCh / 4; ++j) {
+        acc[j].x = fmaf(f, o[u][j].x, acc[j].x);
+        acc[j].y = fmaf(f, o[u][j].y, acc[j].y);
+        acc[j].z = fmaf(f, o[u][j].z, acc[j].z);
+        acc[j].w = fmaf(f, o[u][j].w, acc[j].w);
+      }
     }
   }
-  __syncthreads();   // red is read
-  red[share][row] = L;
+  red[share][row] = make_float2(M, L);
   if (share > 0) {
 #pragma unroll
     for (int j = 0; j < kMergeCh / 4; ++j) racc[share - 1][j][row] = acc[j];
   }
   __syncthreads();
   if (share > 0 || !live) return;
+#pragma unroll
+  for (int u = 1; u < kMergeShares; ++u) M = fmaxf(M, red[u][row].x);
+  float f[kMergeShares];
   L = 0.f;
 #pragma unroll
-  for (int u = 0; u < kMergeShares; ++u) L += red[u][row];
+  for (int u = 0; u < kMergeShares; ++u) {
+    f[u] = exp2f(red[u][row].x - (M == -INFINITY ? 0.f : M));
+    L = fmaf(f[u], red[u][row].y, L);
+  }
   const float inv = L > 0.f ? 1.f / L : 0.f;
   uint32_t pk[kMergeCh / 2];
 #pragma unroll
   for (int j = 0; j < kMergeCh / 4; ++j) {
+    acc[j].x *= f[0]; acc[j].y *= f[0]; acc[j].z *= f[0]; acc[j].w *= f[0];
 #pragma unroll
-    for (int u = 0; u < kMergeShares - 1; ++u) {
-      const float4 v = racc[u][j][row];
-      acc[j].x += v.x; acc[j].y += v.y; acc[j].z += v.z; acc[j].w += v.w;
+    for (int u = 1; u < kMergeShares; ++u) {
+      const float4 v = racc[u - 1][j][row];
+      acc[j].x = fmaf(f[u], v.x, acc[j].x);
+      acc[j].y = fmaf(f[u], v.y, acc[j].y);
+      acc[j].z = fmaf(f[u], v.z, acc[j].z);
+      acc[j].w = fmaf(f[u], v.w, acc[j].w);
     }
     const __nv_bfloat162 x = __floats2bfloat162_rn(acc[j].x * inv, acc[j].y * inv);
     const __nv_bfloat162 y = __floats2bfloat162_rn(acc[j].z * inv, acc[j].w * inv);
