@@ -145,6 +145,16 @@ csa2_status encode_u8_map(const void *base, int64_t rows, int cols, int box_rows
   return CSA2_OK;
 }
 
+// The FP8 rows of a dense attention: boxes of 64 rows x 128 channels.
+csa2_status encode_row_maps(const DenseAttnArgs &a, DenseMaps *m) {
+  csa2_status st = CSA2_OK;
+  if (a.swa_rows)
+    st = encode_u8_map(a.swa_rows, (int64_t)a.B * a.W_cap, a.D, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B, &m->swa);
+  if (st == CSA2_OK && a.sink_rows)
+    st = encode_u8_map(a.sink_rows, (int64_t)a.B * a.sink_cap, a.D, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B, &m->sinks);
+  return st;
+}
+
 csa2_status check_main(const csa2_main_cache *m, bool need_pending) {
   if (!m) return fail(CSA2_ERR_INVALID_ARG, "main cache is NULL");
   if (!m->codes || !m->scales || !m->ik || !m->ik_scale || !m->n_entries)
@@ -753,14 +763,15 @@ csa2_status csa2_prefix_attn_decode(const csa2_page_pool *pool, const int32_t *s
   const int box = prefix_attn_box(pool->page), D = pool->D, DO = D < 256 ? D : 256;
   const int64_t rows = (int64_t)pool->n_pages * pool->page;
   const int join = D == 128 ? 2 : 1;   // entries whose scales make a row of 16 bytes or more
-  CUtensorMap q_map, codes, scales;
-  if ((st = encode_bf16_map(q, (int64_t)B * T_q * H, D, 128, &q_map)) != CSA2_OK ||
+  DenseMaps m{};
+  if ((st = encode_bf16_map(q, (int64_t)B * T_q * H, D, 128, &m.q)) != CSA2_OK ||
       (st = encode_u8_map(pool->codes, rows, D / 2, box, DO / 2,
-                          D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, &codes)) != CSA2_OK ||
+                          D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, &m.codes)) != CSA2_OK ||
       (st = encode_u8_map(pool->scales, rows / join, D / 16 * join, box / join, 16, CU_TENSOR_MAP_SWIZZLE_NONE,
-                          &scales)) != CSA2_OK)
+                          &m.scales)) != CSA2_OK ||
+      (st = encode_row_maps(a, &m)) != CSA2_OK)
     return st;
-  cudaError_t e = launch_prefix_attn(q_map, codes, scales, a, d->sms, reinterpret_cast<cudaStream_t>(stream));
+  cudaError_t e = launch_prefix_attn(m, a, d->sms, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? CSA2_OK : cuda_fail(e, "prefix attention launch");
 }
 
@@ -802,10 +813,15 @@ csa2_status csa2_window_attn(const csa2_swa_cache *swa, const csa2_swa_cache *si
   }
   a.q = q; a.q_pos = q_pos; a.B = swa->B; a.T_q = T_q; a.H = H; a.D = swa->D;
   a.scale = softmax_scale; a.out = out; a.ws = ws; a.status = d->status;
-  CUtensorMap q_map;
-  if ((st = encode_bf16_map(q, (int64_t)a.B * T_q * H, a.D, 128, &q_map)) != CSA2_OK) return st;
-  const auto launch = window_fits_ring(a) ? launch_window_ring : launch_window_attn;
-  const cudaError_t e = launch(q_map, a, d->sms, reinterpret_cast<cudaStream_t>(stream));
+  DenseMaps m{};
+  if ((st = encode_bf16_map(q, (int64_t)a.B * T_q * H, a.D, 128, &m.q)) != CSA2_OK) return st;
+  cudaError_t e;
+  if (window_fits_ring(a)) {
+    e = launch_window_ring(m.q, a, d->sms, reinterpret_cast<cudaStream_t>(stream));
+  } else {
+    if ((st = encode_row_maps(a, &m)) != CSA2_OK) return st;
+    e = launch_window_attn(m, a, d->sms, reinterpret_cast<cudaStream_t>(stream));
+  }
   return e == cudaSuccess ? CSA2_OK : cuda_fail(e, "window attention launch");
 }
 

@@ -98,6 +98,7 @@ struct Segment {
   int seq;                 // pool sequence whose table is read (-1: none)
   int slot;                // partial result's place, -1: straight to the output
   int q0, nq;              // queries of the rows
+  int win_lo, win_hi;      // window tokens, where they are one stretch; else win_hi = -1
   int pos[kMaxQ];          // their token positions
 };
 
@@ -181,6 +182,17 @@ __device__ __forceinline__ bool next_window(const Segment &sg, int window, int c
   }
   *start = lo;
   *end = e < lo + kTile ? e : lo + kTile;
+  return true;
+}
+
+// The same, by arithmetic alone where the windows make one stretch.
+__device__ __forceinline__ bool next_stretch(const Segment &sg, int win_lo, int win_hi, int window, int cur, int lane,
+                                             int *start, int *end) {
+  if (win_hi < 0) return next_window(sg, window, cur, lane, start, end);
+  const int s = cur > win_lo ? cur : win_lo;
+  if (s >= win_hi) return false;
+  *start = s;
+  *end = win_hi - s < kTile ? win_hi : s + kTile;
   return true;
 }
 
@@ -393,6 +405,8 @@ template <int D, int MODE>
 __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_constant__ CUtensorMap q_map,
                                                                  const __grid_constant__ CUtensorMap codes_map,
                                                                  const __grid_constant__ CUtensorMap scales_map,
+                                                                 const __grid_constant__ CUtensorMap swa_map,
+                                                                 const __grid_constant__ CUtensorMap sink_map,
                                                                  const DenseAttnArgs a, const Schedule sc) {
   using F = Cfg<D>;
   constexpr int DO = F::DO, CS = F::CS, NCH = F::NCH, GC = F::GC, NG = F::NG, QT = F::QT, QS = F::QS;
@@ -472,6 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
       // shared memory takes 320 cycles instead of 43)
       const int n_sink = sg.n_sink, n_fp4 = sg.n_fp4, n_tiles = n_sink + n_fp4 + sg.n_win;
       const int key0 = sg.key0, key_lo = sg.key_lo, key_end = sg.key_end;
+      const int win_lo = sg.win_lo, win_hi = sg.win_hi;
       // ---- Q's chunks of shared memory: bf16 -> fp16 in place
       bool ok = all_wait(&S.q_full, seg_i & 1u);
       if constexpr (QS > 0) {
@@ -565,6 +580,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
             }
           }
         } else {
+          // rows of the tile that are keys; what the copies brought behind them: zeros
+          int keys = kTile;
+          if (it < n_sink) keys = key_end - it * kTile;
+          else if (win_hi >= 0) keys = win_hi - win_lo - (it - n_sink - n_fp4) * kTile;
 #pragma unroll 1
           for (int sub = 0; sub < FP8_S; ++sub, ++step) {  // two chunks a step
             const uint32_t st = step % kStages;
@@ -578,6 +597,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
                 rv[u][y] = *reinterpret_cast<const uint4 *>(S.raw[st] + raw_off<kRawRow>(r0 + 8 * y, p4 + 4 * u));
             __syncwarp();
             if (lane == 0) mbar_arrive(&S.raw_empty[st]);
+            if (keys < kTile) {
+#pragma unroll
+              for (int y = 0; y < 2; ++y)
+                if (r0 + 8 * y >= keys) rv[0][y] = rv[1][y] = make_uint4(0, 0, 0, 0);
+            }
             if (sub == 0) ok = all_wait(&S.empty[slot], ph ^ 1u);
             if (!ok) break;
 #pragma unroll
@@ -611,6 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
       const int n_sink = sg.n_sink, n_fp4 = sg.n_fp4, n_tiles = n_sink + n_fp4 + sg.n_win;
       const int half = sg.half;
       const int key0 = sg.key0, key_lo = sg.key_lo, key_end = sg.key_end;
+      const int win_lo = sg.win_lo, win_hi = sg.win_hi;
       const int q = warp & 3, row = 32 * q + lane;
       const uint32_t lrow = tmem + ((uint32_t)(32 * q) << 16);
       const int frow = sg.row0 + row;
@@ -680,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
           page_ahead = pages.next(it + 1 < n_sink + n_fp4, 0);
         } else {
           int s = 0, e = 0;
-          next_window(sg, a.window, wcur, lane, &s, &e);
+          next_stretch(sg, win_lo, win_hi, a.window, wcur, lane, &s, &e);
           wcur = e;
           ja = wlo - s;
           jb = (t < e ? t + 1 : e) - s;
@@ -779,8 +804,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
         tc_fence_after();
       }
       if (MODE == 1 && ok) {
+        // through the ring (no group is in use any more), so that the lanes of
+        // a store lie along a row: a store per lane and row would touch 32 lines
         const float inv = l > 0.f ? vsc / l : 0.f;
-        uint16_t *op = a.out + (size_t)frow * D + half * DO;
 #pragma unroll 1
         for (int c = 0; c < DO; c += 32) {
           uint32_t o[32];
@@ -796,12 +822,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
             const __nv_bfloat162 bv = __floats2bfloat162_rn(x0, x1);
             pk[j] = *reinterpret_cast<const uint32_t *>(&bv);
           }
-          if (live) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<uint4 *>(op + c + 8 * j) = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
-          }
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4 *>(S.kv[0] + sw_off(row, c / 8 + j, kRows)) =
+                make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
         }
+        __syncwarp();   // a warp stores the rows that it has written
+        uint16_t *op = a.out + (size_t)sg.row0 * D + half * DO;
+        const int nrows = sg.nrows;
+#pragma unroll 4
+        for (int i = lane; i < 32 * (DO / 8); i += 32) {
+          const int r = 32 * q + i / (DO / 8), pc = i % (DO / 8);
+          const uint4 v = *reinterpret_cast<const uint4 *>(S.kv[0] + sw_off(r, pc, kRows));
+          if (r < nrows) *reinterpret_cast<uint4 *>(op + (size_t)r * D + 8 * pc) = v;
+        }
+        fence_proxy_async();   // the next segment's Q lands here
       } else if (MODE == 0 && ok) {
         const DenseWs w = dense_ws((long long)sc.units * CS, sc.grid, DO);
         uint8_t *ws = static_cast<uint8_t *>(a.ws);
@@ -875,6 +910,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
         if (more) {
           const int q0 = sg.row0 / a.H, nq = (sg.row0 + sg.nrows - 1) / a.H - q0 + 1;
           int top = -1;   // sinks end where the latest query's window starts
+          int wlo = INT_MAX, whi = -1;
+          bool one = true;   // positions never fall and never skip a token: the windows are one stretch
           for (int i = lane; i < nq; i += 32) {
             int t = a.q_pos[q0 + i];
             if (t > kMaxPos) {   // sums with a tile or a window stay in 32 bits
@@ -886,12 +923,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
               int lo = a.window > 0 ? t - a.window + 1 : t + 1;
               lo = lo < 0 ? 0 : lo;
               top = lo > top ? lo : top;
+              wlo = lo < wlo ? lo : wlo;
+              whi = t + 1 > whi ? t + 1 : whi;
             }
+            if (i > 0) {
+              const int before = a.q_pos[q0 + i - 1];
+              if (before < 0 || t < before || t - before > a.window) one = false;
+            }
+            if (t < 0) one = false;
           }
+          wlo = __reduce_min_sync(0xffffffffu, wlo);
+          whi = __reduce_max_sync(0xffffffffu, whi);
+          one = __all_sync(0xffffffffu, one) && a.window > 0;
           top = __reduce_max_sync(0xffffffffu, top);
           if (lane == 0) {
             sg.q0 = q0;
             sg.nq = nq;
+            sg.win_lo = wlo;
+            sg.win_hi = one ? whi : -1;
             if (MODE == 1) {
               const int n = top < a.n_sink ? top : a.n_sink;
               sg.key_end = n > 0 ? n : 0;
@@ -901,7 +950,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
           __syncwarp();
           if (sg.n_win) {
             int n = 0, cur = 0, s, e;
-            if (a.window > 0)
+            if (one)
+              n = (whi - wlo + kTile - 1) / kTile;
+            else if (a.window > 0)
               while (next_window(sg, a.window, cur, lane, &s, &e)) { ++n; cur = e; }
             __syncwarp();
             if (lane == 0) sg.n_win = n;
@@ -1052,10 +1103,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
               ++scount;
             }
           } else {
+            // rows that follow one another in their plane: a tensor copy of 64
+            // (what lies behind the last key is taken as zeros later)
+            int at = -1;                           // first row
             const uint8_t *base;                   // the rows' sequence
             int row[2] = {-1, -1};
             if (it < n_sink) {
               base = a.sink_rows + (size_t)sg.b * a.sink_cap * D;
+              at = sg.b * a.sink_cap + it * kTile;
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
                 const int key = it * kTile + 32 * y + lane;
@@ -1064,13 +1119,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
             } else {
               base = a.swa_rows + (size_t)sg.b * a.W_cap * D;
               int s = 0, e = 0;
-              next_window(sg, a.window, wcur, lane, &s, &e);
+              next_stretch(sg, sg.win_lo, sg.win_hi, a.window, wcur, lane, &s, &e);
               wcur = e;
+              const int s_row = s % a.W_cap;
+              if (sg.win_hi >= 0 && s_row + (e - s) <= a.W_cap) {
+                at = sg.b * a.W_cap + s_row;
+              } else {
 #pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const int tok = s + 32 * y + lane;
-                if (tok < e) row[y] = tok % a.W_cap;
+                for (int y = 0; y < 2; ++y) {
+                  const int tok = s + 32 * y + lane;
+                  if (tok < e) row[y] = tok % a.W_cap;
+                }
               }
+            }
+            if (at >= 0) {
+              const CUtensorMap *map = it < n_sink ? &sink_map : &swa_map;
+#pragma unroll 1
+              for (int k = 0; k < NCH; k += 2) {   // two chunks a step, in S's order
+                const uint32_t st = scount % kStages;
+                ok = acquire(st);
+                if (!ok) break;
+                if (lane == 0) {
+                  fence_proxy_async();             // a stage that the other form wrote last
+                  mbar_arrive_expect_tx(&S.raw_full[st], kTile * kRawRow);
+                  mbar_arrive_n(&S.raw_full[st], 31);
+                  tma_load_2d(S.raw[st], map, q_chunk(k, half) * 64, at, &S.raw_full[st]);
+                }
+                __syncwarp();
+                ++scount;
+              }
+              continue;
             }
             int rows[16];
             share_rows(0, row[0], rows);
@@ -1244,32 +1322,31 @@ long long prefix_units(int B, int T_q, int H, int D) {
 }
 
 template <int D, int MODE>
-cudaError_t launch_dense(const CUtensorMap &q, const CUtensorMap &codes, const CUtensorMap &scales, const DenseAttnArgs &a, const Schedule &sc,
-                         cudaStream_t s) {
+cudaError_t launch_dense(const DenseMaps &m, const DenseAttnArgs &a, const Schedule &sc, cudaStream_t s) {
   const size_t smem = sizeof(DenseSmem<D>) + 1024;
   static_assert(sizeof(DenseSmem<D>) + 1024 <= 232448, "shared memory");
   static_assert(Cfg<D>::QT * kRows <= Cfg<D>::NG * Cfg<D>::GC * kTile, "Q's staging in the ring");
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t e = allow_smem_once(attn_dense_kernel<D, MODE>, smem, &allowed);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_dense_kernel<D, MODE>, dim3(sc.grid), dim3(kThreads), smem, s, dim3(1, 1, 1), q, codes, scales, a, sc);
+  return launch_pdl(attn_dense_kernel<D, MODE>, dim3(sc.grid), dim3(kThreads), smem, s, dim3(1, 1, 1), m.q, m.codes,
+                    m.scales, m.swa, m.sinks, a, sc);
 }
 
 template <int D>
-cudaError_t launch_prefix_t(const CUtensorMap &q, const CUtensorMap &codes, const CUtensorMap &scales, const DenseAttnArgs &a, int sms, cudaStream_t s) {
+cudaError_t launch_prefix_t(const DenseMaps &m, const DenseAttnArgs &a, int sms, cudaStream_t s) {
   const Schedule sc = make_schedule(a, Cfg<D>::CS, sms);
-  cudaError_t e = launch_dense<D, 0>(q, codes, scales, a, sc, s);
+  cudaError_t e = launch_dense<D, 0>(m, a, sc, s);
   if (e != cudaSuccess) return e;
   return launch_pdl(attn_dense_merge_kernel<D>, dim3(sc.rt_sh, D / kMergeCh), dim3(kRows * kMergeShares), 0, s, dim3(1, 1, 1), a, sc);
 }
 
 template <int D>
-cudaError_t launch_window_t(const CUtensorMap &q, const DenseAttnArgs &a, int sms, cudaStream_t s) {
+cudaError_t launch_window_t(const DenseMaps &m, const DenseAttnArgs &a, int sms, cudaStream_t s) {
   Schedule sc = make_schedule(a, Cfg<D>::CS, sms);
   const long long units = (long long)a.B * sc.rt_own * Cfg<D>::CS;
   if (units < sc.grid) sc.grid = (int)units;
-  const CUtensorMap none{};   // no entries
-  return launch_dense<D, 1>(q, none, none, a, sc, s);
+  return launch_dense<D, 1>(m, a, sc, s);
 }
 
 }  // namespace
@@ -1277,20 +1354,19 @@ cudaError_t launch_window_t(const CUtensorMap &q, const DenseAttnArgs &a, int sm
 size_t prefix_attn_workspace_bytes(int B, int T_q, int H, int D, int sms) {
   return dense_ws(prefix_units(B, T_q, H, D), sms, D < 256 ? D : 256).bytes;
 }
-cudaError_t launch_prefix_attn(const CUtensorMap &q, const CUtensorMap &codes, const CUtensorMap &scales,
-                               const DenseAttnArgs &a, int sms, cudaStream_t s) {
+cudaError_t launch_prefix_attn(const DenseMaps &m, const DenseAttnArgs &a, int sms, cudaStream_t s) {
   switch (a.D) {
-    case 128: return launch_prefix_t<128>(q, codes, scales, a, sms, s);
-    case 256: return launch_prefix_t<256>(q, codes, scales, a, sms, s);
-    default: return launch_prefix_t<512>(q, codes, scales, a, sms, s);
+    case 128: return launch_prefix_t<128>(m, a, sms, s);
+    case 256: return launch_prefix_t<256>(m, a, sms, s);
+    default: return launch_prefix_t<512>(m, a, sms, s);
   }
 }
 size_t window_attn_workspace_bytes(int, int, int, int, int, int, int) { return 0; }
-cudaError_t launch_window_attn(const CUtensorMap &q, const DenseAttnArgs &a, int sms, cudaStream_t s) {
+cudaError_t launch_window_attn(const DenseMaps &m, const DenseAttnArgs &a, int sms, cudaStream_t s) {
   switch (a.D) {
-    case 128: return launch_window_t<128>(q, a, sms, s);
-    case 256: return launch_window_t<256>(q, a, sms, s);
-    default: return launch_window_t<512>(q, a, sms, s);
+    case 128: return launch_window_t<128>(m, a, sms, s);
+    case 256: return launch_window_t<256>(m, a, sms, s);
+    default: return launch_window_t<512>(m, a, sms, s);
   }
 }
 

@@ -262,14 +262,17 @@ size_t prefix_attn_workspace_bytes(int B, int T_q, int H, int D, int sms);
 // Entries that a copy of the pool's planes takes: the largest of 16, 32 and 64
 // that divides the page.
 inline int prefix_attn_box(int page) { return page % 64 == 0 ? 64 : (page % 32 == 0 ? 32 : 16); }
-// q: rows of D bf16, boxes of 128 rows x 64 channels in the 128B swizzle.
-// codes, scales: maps of the pool's planes, rows = entries (two entries for the
-// scales of D 128); boxes of prefix_attn_box entries x 256 channels at most, the
-// codes in the swizzle of the box's width.
-cudaError_t launch_prefix_attn(const CUtensorMap &q, const CUtensorMap &codes, const CUtensorMap &scales,
-                               const DenseAttnArgs &a, int sms, cudaStream_t s);
+struct DenseMaps {
+  CUtensorMap q;            // rows of D bf16, boxes of 128 rows x 64 channels in the 128B swizzle
+  // the pool's planes, rows = entries (two entries for the scales of D 128);
+  // boxes of prefix_attn_box entries x 256 channels at most, the codes in the
+  // swizzle of the box's width
+  CUtensorMap codes, scales;
+  CUtensorMap swa, sinks;   // rows of D bytes, boxes of 64 rows x 128 channels in the 128B swizzle
+};
+cudaError_t launch_prefix_attn(const DenseMaps &m, const DenseAttnArgs &a, int sms, cudaStream_t s);
 size_t window_attn_workspace_bytes(int B, int T_q, int H, int D, int window, int n_sink, int sms);
-cudaError_t launch_window_attn(const CUtensorMap &q, const DenseAttnArgs &a, int sms, cudaStream_t s);
+cudaError_t launch_window_attn(const DenseMaps &m, const DenseAttnArgs &a, int sms, cudaStream_t s);
 // The resident form (attn_window.cu), for the launches it takes.
 bool window_fits_ring(const DenseAttnArgs &a);
 cudaError_t launch_window_ring(const CUtensorMap &q_map, const DenseAttnArgs &a, int sms, cudaStream_t s);
