@@ -317,9 +317,10 @@ def test_compact_closes_every_hole(n_pages, live):
 # --------------------------------------------------------------------------- prefix attention
 
 
-def paged_batch(seed, D, page, n_shared, lens, n_seq_extra=1, m=1):
+def paged_batch(seed, D, page, n_shared, lens, n_seq_extra=1, m=1, poison=False):
     """A pool whose sequences agree on the first n_shared entries and own the
-    rest, in shuffled pages; (pool, seq, entry values per batch row)."""
+    rest, in shuffled pages; (pool, seq, entry values per batch row).  `poison`:
+    every byte that no sequence's entry owns is 0xFF (a scale of NaN)."""
     g, rng = gen(seed), np.random.default_rng(seed)
     B, S = len(lens), len(lens) + n_seq_extra
     full = min(n_shared, min([max(n, 0) for n in lens if n >= n_shared] or [0])) // page
@@ -355,6 +356,13 @@ def paged_batch(seed, D, page, n_shared, lens, n_seq_extra=1, m=1):
         pg = torch.as_tensor(table[seq[b]][: -(-n // page)].astype(np.int64), device="cuda")
         values.append(fp4_values(pool.codes[pg].flatten(0, 1)[:n], pool.scales[pg].flatten(0, 1)[:n]) if n else
                       torch.zeros(0, D, dtype=torch.float64, device="cuda"))
+    if poison:
+        owned = torch.zeros(n_pages, page, dtype=torch.bool, device="cuda")
+        for b, n in enumerate(lens):
+            for k in range(-(-n // page)):
+                owned[int(table[seq[b], k]), : n - k * page] = True
+        pool.codes[~owned] = 255
+        pool.scales[~owned] = 255
     return pool, i32(seq), values
 
 
@@ -364,6 +372,17 @@ def window_keys(rows_b, scale, t, window):
     return rows_b.view(torch.float8_e4m3fn).double()[tok % W_cap] * scale
 
 
+def poison_rows(rows, q_pos, window):
+    """The ring's rows that no query sees: all NaN."""
+    W_cap = rows.shape[1]
+    for b, ts in enumerate(q_pos):
+        seen = torch.zeros(W_cap, dtype=torch.bool, device="cuda")
+        for t in ts:
+            if t >= 0 and window:
+                seen[torch.arange(max(0, t - window + 1), t + 1, device="cuda") % W_cap] = True
+        rows[b, ~seen] = 255
+
+
 def guarded(shape):
     """An output with marked rows before and behind it."""
     n = math.prod(shape)
@@ -371,15 +390,18 @@ def guarded(shape):
     return buf, buf[1024:1024 + n].view(shape)
 
 
-def run_prefix(D, H, T, page, n_shared, lens, window, m=1, seed=0, s_swa=0.75, q_pos=None, scale=None, spread=1.0):
+def run_prefix(D, H, T, page, n_shared, lens, window, m=1, seed=0, s_swa=0.75, q_pos=None, scale=None, spread=1.0,
+               poison=False):
     g = gen(seed + 77)
-    pool, seq, values = paged_batch(seed, D, page, n_shared, lens, m=m)
+    pool, seq, values = paged_batch(seed, D, page, n_shared, lens, m=m, poison=poison)
     B = len(lens)
     q = (torch.randn(B, T, H, D, generator=g, device="cuda") * spread).to(torch.bfloat16)
     if q_pos is None:   # the last entry of a sequence was completed by its last query token
         q_pos = [[max(-1, m * n - T + j) for j in range(T)] for n in lens]
     W_cap = max(1, window + T + 3)
     rows = e4m3_rows(g, B, W_cap, D)
+    if poison:
+        poison_rows(rows, q_pos, window)
     swa = C.SwaCache.of(rows, scale=s_swa, window=window) if window else None
     buf, out = guarded((B, T, H, D))
     scale = scale or 1.0 / math.sqrt(D)
@@ -411,6 +433,25 @@ def run_prefix(D, H, T, page, n_shared, lens, window, m=1, seed=0, s_swa=0.75, q
 ])
 def test_prefix_attention(D, H, T, page, n_shared, lens, window):
     run_prefix(D, H, T, page, n_shared, lens, window, seed=D + H + page)
+
+
+@pytest.mark.parametrize("D,H,T,page,n_shared,lens,window", [
+    (128, 8, 1, 16, 300, [340, 301, 517], 128),
+    (128, 3, 2, 48, 0, [1, 0, 49, 130], 0),
+    (256, 20, 3, 32, 100, [101, 164, 333], 40),
+    (256, 64, 1, 64, 130, [191, 200], 0),
+    (512, 64, 1, 128, 129, [130, 700], 128),
+    (512, 16, 2, 80, 77, [78, 240], 9),
+])
+def test_prefix_attention_among_bytes_of_nan(D, H, T, page, n_shared, lens, window):
+    run_prefix(D, H, T, page, n_shared, lens, window, seed=D + H, poison=True)
+
+
+@pytest.mark.parametrize("scale", [-0.05, 1e-30])
+def test_attention_by_a_negative_and_a_tiny_scale(scale):
+    run_prefix(256, 20, 2, 32, 70, [90, 200], 40, seed=4, scale=scale)
+    run_window(2, 5, 8, 512, 128, 4, 300, seed=5, scale=scale)
+    run_window(1, 5, 8, 256, 400, 4, 300, seed=6, scale=scale)
 
 
 def test_prefix_attention_long_and_many_rows():
@@ -475,7 +516,8 @@ def test_prefix_attention_equals_the_sparse_attention_over_all_entries():
 # --------------------------------------------------------------------------- window attention
 
 
-def run_window(B, T, H, D, window, n_sink, start, seed=0, s_swa=0.75, s_sink=1.5, q_pos=None, spread=1.0, scale=None):
+def run_window(B, T, H, D, window, n_sink, start, seed=0, s_swa=0.75, s_sink=1.5, q_pos=None, spread=1.0, scale=None,
+               poison=False):
     g = gen(seed + 13)
     W_cap = max(1, window + T - 1 + seed % 5)
     rows = e4m3_rows(g, B, W_cap, D)
@@ -485,6 +527,11 @@ def run_window(B, T, H, D, window, n_sink, start, seed=0, s_swa=0.75, s_sink=1.5
     q = (torch.randn(B, T, H, D, generator=g, device="cuda") * spread).to(torch.bfloat16)
     if q_pos is None:
         q_pos = [[start + 3 * b + j for j in range(T)] for b in range(B)]
+    if poison:
+        poison_rows(rows, q_pos, window)
+        for b in range(B):
+            first = max([max(0, t - window + 1) if window else t + 1 for t in q_pos[b] if t >= 0] or [0])
+            sink_rows[b, min(n_sink, first):] = 255
     buf, out = guarded((B, T, H, D))
     scale = scale or 1.0 / math.sqrt(D)
     C.csa2_window_attn(swa, sinks, q, i32(q_pos), scale, out)
@@ -520,6 +567,19 @@ def run_window(B, T, H, D, window, n_sink, start, seed=0, s_swa=0.75, s_sink=1.5
 ])
 def test_window_attention(B, T, H, D, window, n_sink, start):
     run_window(B, T, H, D, window, n_sink, start, seed=T + H)
+
+
+@pytest.mark.parametrize("B,T,H,D,window,n_sink,start", [
+    (2, 1, 8, 128, 128, 4, 1000),
+    (2, 37, 64, 512, 128, 4, 0),
+    (3, 5, 20, 256, 33, 7, 2),
+    (1, 40, 5, 256, 333, 16, 320),
+    (2, 9, 64, 512, 1024, 64, 5000),
+    (2, 33, 4, 128, 700, 9, 650),
+    (1, 3, 64, 512, 200, 0, 0),
+])
+def test_window_attention_among_rows_of_nan(B, T, H, D, window, n_sink, start):
+    run_window(B, T, H, D, window, n_sink, start, seed=T + D, poison=True)
 
 
 def test_window_attention_padded_and_unordered_queries():
