@@ -471,8 +471,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
     const __half2 hv = __floats2half2_rn(bf16_to_f32(w & 0xFFFFu) * qsign, bf16_to_f32(w >> 16) * qsign);
     return *reinterpret_cast<const uint32_t *>(&hv);
   };
+  // A converged warp's wait, polled by all its lanes: one that lane 0 polls for
+  // the others leaves it behind at times, and the tcgen05 instructions that
+  // follow have to be met by all lanes at once.
   auto all_wait = [&](uint64_t *bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort)) != 0;
+    const bool w_ok = __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort)) != 0;
+    __syncwarp();
+    return w_ok;
   };
   uint32_t gcount = 0, tcount = 0;   // ring groups and tiles so far (each role advances them alike)
   uint32_t scount = 0;               // raw steps so far (load and dequantise)
@@ -513,6 +518,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
       };
+      // A step's bytes.  The stage's step before may be the other team's: that
+      // it has been consumed comes first, since the copies land in any order
+      // and a wait for this step's phase, met in the phase before the last,
+      // would pass at once.  (The one before that has been consumed: this team
+      // has seen a step at most three back, which was loaded after it.)
+      auto raw_wait = [&](uint32_t step) -> bool {
+        const uint32_t st = step % kStages, ph = (step / kStages) & 1u;
+        return all_wait(&S.raw_empty[st], ph ^ 1u) && all_wait(&S.raw_full[st], ph);
+      };
       constexpr int FP8_S = GC / 2;                        // steps of a group of FP8 rows
 #pragma unroll 1
       for (int it = 0; it < n_tiles && ok; ++it) {
@@ -528,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
         uint8_t *kv = S.kv[slot];
         if (fp4) {
           const uint32_t st = step % kStages;
-          ok = all_wait(&S.raw_full[st], (step / kStages) & 1u);
+          ok = raw_wait(step);
           if (!ok) break;
           constexpr int NU = GC / 2;                       // pieces of 32 channels per key
           uint4 rv[NU][2];
@@ -587,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
 #pragma unroll 1
           for (int sub = 0; sub < FP8_S; ++sub, ++step) {  // two chunks a step
             const uint32_t st = step % kStages;
-            ok = all_wait(&S.raw_full[st], (step / kStages) & 1u);
+            ok = raw_wait(step);
             if (!ok) break;
             uint4 rv[2][2];
 #pragma unroll
@@ -675,11 +689,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
       int wlo = t - a.window + 1;
       if (wlo < 0) wlo = 0;
       const int snk = MODE == 1 && t >= 0 ? (a.window > 0 ? wlo : t + 1) : 0;   // sinks below this token
-      auto warp_wait = [&](uint64_t *bar, uint32_t parity) {
-        int w_ok = 1;
-        if (lane == 0) w_ok = wait_or_abort(bar, parity, abort);
-        return __shfl_sync(0xffffffffu, w_ok, 0) != 0;
-      };
       // Pages of the next FP4 tile (lane = box of the tile), looked up a tile
       // ahead and judged when the tile comes: a slot without a page gave zeros,
       // its keys are hidden.
@@ -715,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
         const bool whole = __all_sync(0xffffffffu, ja <= 0 && jb >= kTile) && badp == 0;
         const uint32_t buf = tc & 1u, ph = (tc >> 1) & 1u;
         const uint32_t scol = lrow + kColS + buf * kTile;
-        ok = warp_wait(&S.s_full[buf], ph);
+        ok = all_wait(&S.s_full[buf], ph);
         if (!ok) break;
         tc_fence_after();
         // logits in base 2: lsc x S; never 0, so that a hidden key's -inf stays
@@ -778,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
         const float f = al * conv;
         if (it > 0 && __any_sync(0xffffffffu, f != 1.f)) {
           const uint32_t pt = tc - 1;                      // O of the tile before is complete
-          ok = warp_wait(&S.pv_done[pt & 1u], (pt >> 1) & 1u);
+          ok = all_wait(&S.pv_done[pt & 1u], (pt >> 1) & 1u);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
@@ -800,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
       // ================================================ the segment's result
       if (ok && n_tiles > 0) {
         const uint32_t pt = tcount + n_tiles - 1;
-        ok = warp_wait(&S.pv_done[pt & 1u], (pt >> 1) & 1u);
+        ok = all_wait(&S.pv_done[pt & 1u], (pt >> 1) & 1u);
         tc_fence_after();
       }
       if (MODE == 1 && ok) {

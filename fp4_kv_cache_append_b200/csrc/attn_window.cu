@@ -146,8 +146,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
   // this pass's descriptor; every role takes all passes in order
   uint32_t pi = 0;
   auto next_pass = [&]() -> bool {
-    return __all_sync(0xffffffffu, wait_or_abort(&S.pass_full[pi % kPasses], (pi / kPasses) & 1u, abort)) != 0 &&
-           S.pass[pi % kPasses].more != 0;
+    const bool w_ok = __all_sync(0xffffffffu, wait_or_abort(&S.pass_full[pi % kPasses], (pi / kPasses) & 1u, abort)) != 0;
+    __syncwarp();   // (as in all_wait)
+    return w_ok && S.pass[pi % kPasses].more != 0;
   };
   auto free_pass = [&]() {   // the descriptor is not needed any more (one arrival per warp)
     __syncwarp();
@@ -210,19 +211,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
   };
   // Until `n` passes are complete (their O products: nothing reads their keys any more).
   auto wait_done = [&](int n) -> bool {
-    int w_ok = 1;
-    if (n > 0 && lane == 0) {
-      const volatile int *done = &S.passes_done;
-      uint32_t i = 0;
-      while (*done < n) {
-        if (++i >= kWaitLimit || *abort) { w_ok = 0; *abort = 1; break; }
-        __nanosleep(64);
+    const volatile int *done = &S.passes_done;
+    for (uint32_t i = 0; n > 0 && *done < n; ++i) {   // (all lanes: see all_wait)
+      if (i >= kWaitLimit || *abort) {
+        *abort = 1;
+        return false;
       }
+      __nanosleep(64);
     }
-    return __shfl_sync(0xffffffffu, w_ok, 0) != 0;
+    return true;
   };
+  // A converged warp's wait, polled by all its lanes: one that lane 0 polls for
+  // the others leaves it behind at times, and the tcgen05 instructions that
+  // follow have to be met by all lanes at once.
   auto all_wait = [&](uint64_t *bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort)) != 0;
+    const bool w_ok = __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort)) != 0;
+    __syncwarp();
+    return w_ok;
   };
 
   if (warp < kEpiWarp0) {

@@ -447,6 +447,34 @@ def test_prefix_attention_among_bytes_of_nan(D, H, T, page, n_shared, lens, wind
     run_prefix(D, H, T, page, n_shared, lens, window, seed=D + H, poison=True)
 
 
+@pytest.mark.parametrize("form", ["prefix 512", "prefix 128", "window 256 of 333", "window 512 of 128"])
+def test_attention_launched_back_to_back_gives_the_same_bits(form):
+    """Thousands of launches that overlap at their ends: the stages that the
+    teams of a block share are met in every order of arrival."""
+    kind, D, *rest = form.split()
+    D, B, H, g = int(D), 4, 16, gen(31)
+    scale = 1.0 / math.sqrt(D)
+    if kind == "prefix":
+        pool, seq, _ = paged_batch(3, D, 64, 700, [1100, 900, 701, 1300])
+        swa = C.SwaCache.of(e4m3_rows(g, B, 140, D), scale=1.0, window=128)
+        q = torch.randn(B, 1, H, D, generator=g, device="cuda").to(torch.bfloat16)
+        pos, ws = i32([[2000]] * B), C.workspace(C.csa2_prefix_attn_workspace_size(B, 1, H, D))
+        call = lambda out: C.csa2_prefix_attn_decode(pool, seq, 700, swa, q, pos, scale, out, ws=ws)   # noqa: E731
+    else:
+        T, W = 130, int(rest[1])
+        swa = C.SwaCache.of(e4m3_rows(g, B, W + T + 30, D), scale=1.0, window=W)
+        q = torch.randn(B, T, H, D, generator=g, device="cuda").to(torch.bfloat16)
+        pos = i32([[500 + j for j in range(T)]] * B)
+        call = lambda out: C.csa2_window_attn(swa, None, q, pos, scale, out)   # noqa: E731
+    first, again = torch.empty_like(q), torch.empty_like(q)
+    call(first)
+    for i in range(4000):
+        call(again)
+        if i % 500 == 499:
+            assert torch.equal(first, again), i
+    assert C.csa2_device_status() == 0
+
+
 @pytest.mark.parametrize("scale", [-0.05, 1e-30])
 def test_attention_by_a_negative_and_a_tiny_scale(scale):
     run_prefix(256, 20, 2, 32, 70, [90, 200], 40, seed=4, scale=scale)
