@@ -10,7 +10,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "common.cuh"
-#include "kernels.h"
+#include "kernels_paged.h"
 
 namespace csa2 {
 
@@ -816,7 +816,7 @@ csa2_status csa2_window_attn(const csa2_swa_cache *swa, const csa2_swa_cache *si
   DenseMaps m{};
   if ((st = encode_bf16_map(q, (int64_t)a.B * T_q * H, a.D, 128, &m.q)) != CSA2_OK) return st;
   cudaError_t e;
-  if (window_fits_ring(a)) {
+  if (window_takes_ring(a, d->sms)) {
     e = launch_window_ring(m.q, a, d->sms, reinterpret_cast<cudaStream_t>(stream));
   } else {
     if ((st = encode_row_maps(a, &m)) != CSA2_OK) return st;

@@ -12,9 +12,9 @@
 //
 // One persistent block per SM; keys in tiles of 64.  Warp roles, handing work
 // over through mbarriers:
-//   warp 13     loads (cp.async) the raw bytes of a step (256 channels of a
-//               tile's FP4 codes and scales, or 128 of its FP8 rows), whatever
-//               pages its keys lie in, into one of three stages
+//   warp 13     loads: Q of the unit; then, by tensor copies, the raw bytes of a
+//               step (256 channels of a tile's FP4 codes and scales, page by page,
+//               or 128 of its FP8 rows) into one of three stages
 //   warps 0-7   dequantise, exactly, to fp16 into a ring of chunk groups
 //               (64-channel chunks, K-major, 128B swizzle); two teams of four
 //               warps take the groups in turn.  The chunks that only S needs
@@ -27,14 +27,14 @@
 //               i + 1 runs during tile i's softmax, O of tile i as soon as its P
 //               is there
 //   warp 15     writes the next segment (see below) while this one runs
-// Up to four chunks of Q (256 channels) are kept in tensor memory as the A
-// operand, the rest in shared memory: shared-memory bandwidth bounds the S
-// product (128 rows of A and 64 of B per K step of 16 take 48 cycles against
-// 32 of the tensor core), and the room it leaves holds the stages and a fourth
-// ring group (with three, the fetch of a tile waits for the O product of the
-// tile two before it).  S has two buffers, since about 700 cycles pass between
-// the last MMA of a tile and the first of the next that waited for it; P
-// replaces its tile's S.
+// Q lands as bf16 (its first chunks where the ring will be, the rest in place)
+// and is converted by the softmax and the dequantising warps.  Up to four chunks
+// of Q (256 channels) go to tensor memory as the A operand, the rest stays in
+// shared memory: a K step of 16 with Q in tensor memory takes 33 cycles, with Q
+// in shared memory 49 (128 rows of A and 64 of B are read), and the room it
+// leaves holds the stages and a fourth ring group (with three, the fetch of a
+// tile waits for the O product of the tile two before it).  S has two buffers;
+// P replaces its tile's S.
 // Rows are given by unit (128 rows x a list of keys); a unit's key list is
 // split over blocks wherever the even division of all tiles over the SMs cuts
 // it, each part leaving (O, max, sum) in the workspace for a merge kernel.
@@ -43,9 +43,26 @@
 // Each role runs its own loop over the block's segments and meets the others
 // at named barriers, so that the registers can be divided between the roles.
 // Every wait is bounded: one that gives up flags the device status and stops
-// every role; issued MMAs are drained and TMEM freed before the block exits.
+// every role; issued MMAs and copies are drained and TMEM freed before the block
+// exits.
+//
+// What bounds it (D 512, H 64, 32 sequences of one token, 65,536 shared entries
+// and 512 to 1,024 own ones: 337 us alone, 369 us in a long loop, where the power
+// limit holds the SMs near 1.6 GHz; 755 TFLOP/s of the 4 D FLOP per row and
+// key): shared memory.  A tile of 64 keys and a channel half moves 260 KB through
+// it (S with Q in shared memory 96, in tensor memory 32, O 32, the fp16 keys
+// written 64, the raw bytes in and out 36; the bank counters say the same): 2,030
+// cycles at the 128 bytes a cycle that the S product reaches, of 2,400 measured;
+// the tensor core is busy for 1,830 of them.  For D 128 and 256 all of Q is in
+// tensor memory and the softmax's own chain (about 1,650 cycles a tile: 64
+// exponentials on a scheduler's pipe take 512) is the longest.
+// Loads with a copy instruction per 16 bytes (cp.async) took 2,560 cycles of the
+// loading warp per tile, more than the tile itself: 424 us against 384 us then.
+// A softmax split over two threads per row needs an exchange through shared
+// memory, where a load beside the S product takes 320 cycles instead of 43: 440
+// us against 384 us then.
 #include "attn_dense.cuh"
-#include "kernels.h"
+#include "kernels_paged.h"
 
 namespace csa2 {
 
@@ -63,13 +80,15 @@ constexpr int kSchedWarp = 15;               // writes the next segment
 // logits stay in registers; a spill would go to L2, shared memory takes all of
 // the L1's room).  Their sum is at most the launch's 4 x 128.
 constexpr int kRegsFetch = 88, kRegsSoftmax = 208, kRegsMma = 128;
-constexpr int kLoadWarp = 13;                // loader: lane = keys lane and lane + 32
+constexpr int kLoadWarp = 13;                // loader
 constexpr int kPvWarp = 14;                  // MMA issuer of O (kMmaWarp: of S)
 constexpr int kStages = 3;                   // raw steps in flight or in use
 // A stage: 64 rows of 128 bytes (codes, 64 bytes for D 128, or FP8 values),
 // then 64 rows of scales (16 bytes, 8 for D 128).
 constexpr int kRawRow = 128, kRawSc = kTile * kRawRow, kRawBytes = kRawSc + kTile * 16;
-constexpr int kUnitCost = 8;                 // see Schedule::ov: 12k cycles at 2.7k a tile (D 512)
+// A unit's start and end in tiles (see Schedule::ov): the case above takes 427 us
+// with 2, 363 with 5, 343 with 8, 345 with 10 and 349 with 16.
+constexpr int kUnitCost = 8;
 constexpr float kLazy = 15.0f;               // log2 headroom of P below fp16's 65,504
 // TMEM columns: O, S of two tiles (each later its P), Q's first chunks
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 384, kTmemCols = 512;

