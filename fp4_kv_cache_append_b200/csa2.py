@@ -431,13 +431,15 @@ def csa2_pages_workspace_size(pool: PagePool, n: int) -> int:
     return int(lib().csa2_pages_workspace_size(ctypes.byref(d), int(n)))
 
 
-def _ws_for(ws, nbytes: int, device, stream):
-    """A caller workspace, or a fresh one that the call's own stream may keep
-    using after this function's reference to it is gone."""
-    if ws is None and nbytes:
-        ws = workspace(nbytes, device)
-        if stream is not None and ws.is_cuda:
-            ws.record_stream(torch.cuda.ExternalStream(_stream(stream), device=ws.device))
+def _own_ws(nbytes: int, device, stream):
+    """A fresh workspace that the call's own stream may keep using after this
+    function's reference to it is gone.  (Asked for only without a caller's: the
+    library checks the size of that one.)"""
+    if not nbytes:
+        return None
+    ws = workspace(nbytes, device)
+    if stream is not None and ws.is_cuda:
+        ws.record_stream(torch.cuda.ExternalStream(_stream(stream), device=ws.device))
     return ws
 
 
@@ -451,7 +453,8 @@ def _list(t, n: int, what: str):
 def csa2_pages_append(pool: PagePool, src: MainCache, seq, at=None, first=None, ws=None, stream=None):
     """Entries first[i] .. src.n_entries[i] - 1 of src's row i follow the first
     at[i] entries of pool sequence seq[i]."""
-    ws = _ws_for(ws, csa2_pages_workspace_size(pool, src.B), pool.codes.device, stream)
+    if ws is None:
+        ws = _own_ws(csa2_pages_workspace_size(pool, src.B), pool.codes.device, stream)
     _check(lib().csa2_pages_append(ctypes.byref(pool.desc()), ctypes.byref(src.desc()), _list(first, src.B, "first"),
                                    _list(seq, src.B, "seq"), _list(at, src.B, "at"), _ptr(ws), _nbytes(ws),
                                    _stream(stream)))
@@ -460,14 +463,16 @@ def csa2_pages_append(pool: PagePool, src: MainCache, seq, at=None, first=None, 
 def csa2_pages_fork(pool: PagePool, parent, child, ws=None, stream=None):
     """child[i] becomes a copy of parent[i] that shares its pages (-1: emptied)."""
     n = child.numel()
-    ws = _ws_for(ws, csa2_pages_workspace_size(pool, n), pool.codes.device, stream)
+    if ws is None:
+        ws = _own_ws(csa2_pages_workspace_size(pool, n), pool.codes.device, stream)
     _check(lib().csa2_pages_fork(ctypes.byref(pool.desc()), _list(parent, n, "parent"), _list(child, n, "child"), n,
                                  _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
 def csa2_pages_compact(pool: PagePool, n_live=None, ws=None, stream=None):
     """Pages in use move below all free ones; n_live [1] gets their number."""
-    ws = _ws_for(ws, csa2_pages_workspace_size(pool, 1), pool.codes.device, stream)
+    if ws is None:
+        ws = _own_ws(csa2_pages_workspace_size(pool, 1), pool.codes.device, stream)
     _check(lib().csa2_pages_compact(ctypes.byref(pool.desc()), _ptr(n_live, torch.int32), _ptr(ws), _nbytes(ws),
                                     _stream(stream)))
 
@@ -490,7 +495,8 @@ def csa2_prefix_attn_decode(pool: PagePool, seq, n_shared: int, swa: SwaCache | 
     seq [B] (the first n_shared the same for all) and to the window rows."""
     B = seq.numel()
     T_q, H = _queries(q, q_pos, out, B, pool.D)
-    ws = _ws_for(ws, csa2_prefix_attn_workspace_size(B, T_q, H, pool.D), out.device, stream)
+    if ws is None:
+        ws = _own_ws(csa2_prefix_attn_workspace_size(B, T_q, H, pool.D), out.device, stream)
     sd = ctypes.byref(swa.desc()) if swa is not None else None
     _check(lib().csa2_prefix_attn_decode(ctypes.byref(pool.desc()), _ptr(seq, torch.int32), int(n_shared), sd,
                                          _ptr(q, torch.bfloat16), _ptr(q_pos, torch.int32), B, T_q, H,
@@ -507,7 +513,8 @@ def csa2_window_attn(swa: SwaCache, sinks: SwaCache | None, q, q_pos, softmax_sc
     sinks.window tokens (rows of `sinks`) before them."""
     T_q, H = _queries(q, q_pos, out, swa.B, swa.D)
     n_sink = sinks.window if sinks is not None else 0
-    ws = _ws_for(ws, csa2_window_attn_workspace_size(swa.B, T_q, H, swa.D, swa.window, n_sink), out.device, stream)
+    if ws is None:
+        ws = _own_ws(csa2_window_attn_workspace_size(swa.B, T_q, H, swa.D, swa.window, n_sink), out.device, stream)
     kd = ctypes.byref(sinks.desc()) if sinks is not None else None
     _check(lib().csa2_window_attn(ctypes.byref(swa.desc()), kd, _ptr(q, torch.bfloat16), _ptr(q_pos, torch.int32), T_q,
                                   H, float(softmax_scale), _ptr(out, torch.bfloat16), _ptr(ws), _nbytes(ws),

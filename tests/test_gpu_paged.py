@@ -292,6 +292,29 @@ def test_fork_takes_all_parents_as_they_stood():
         ref.same(pool, f"{parent} -> {child}")
 
 
+@pytest.mark.parametrize("n,S,M", [(1, 1, 1), (7, 9, 33), (255, 256, 3), (256, 300, 256), (257, 300, 5), (9, 12, 4096),
+                                   (9, 12, 4097), (64, 80, 1025), (1000, 1100, 2)])
+def test_fork_of_lists_of_any_length(n, S, M):
+    """Either side of what one cluster takes: random tables, parents, children,
+    a few of them out of range or listed twice."""
+    rng = np.random.default_rng(n + M)
+    pool = C.PagePool(500, 16, S, M, 128)
+    lens = rng.integers(0, M + 1, S)
+    table = np.where(np.arange(M)[None] < lens[:, None], rng.integers(0, 500, (S, M)), -1).astype(np.int32)
+    pool.table, pool.n_entries = i32(table), i32(16 * lens)
+    refs = np.zeros(500, np.int32)
+    np.add.at(refs, table[table >= 0], 1)
+    pool.refs = i32(refs)
+    ref = Model(pool)
+    parent, child = rng.integers(-1, S, n), rng.permutation(S)[:n]
+    if n > 5:
+        child[n - 1], parent[2], child[4] = child[1], S, -1
+    C.csa2_pages_fork(pool, i32(parent), i32(child))
+    ref.fork(parent.tolist(), child.tolist())
+    ref.same(pool)
+    assert C.csa2_device_status() == (C.DEV_BAD_SEQUENCE if n > 5 else 0)
+
+
 @pytest.mark.parametrize("n_pages,live", [(1, 0), (1, 1), (4, 4), (5, 2), (5000, 1700), (9001, 9000)])
 def test_compact_closes_every_hole(n_pages, live):
     rng = np.random.default_rng(n_pages)
