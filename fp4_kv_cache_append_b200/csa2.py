@@ -432,15 +432,17 @@ def csa2_pages_workspace_size(pool: PagePool, n: int) -> int:
 
 
 def _own_ws(nbytes: int, device, stream):
-    """A fresh workspace that the call's own stream may keep using after this
-    function's reference to it is gone.  (Asked for only without a caller's: the
+    """A fresh workspace, made on the call's own stream, so that its memory goes
+    to others only behind this call.  (Asked for only without a caller's: the
     library checks the size of that one.)"""
-    if not nbytes:
+    if nbytes == 0:
         return None
-    ws = workspace(nbytes, device)
-    if stream is not None and ws.is_cuda:
-        ws.record_stream(torch.cuda.ExternalStream(_stream(stream), device=ws.device))
-    return ws
+    if stream is None or not _device_required():
+        return workspace(nbytes, device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=device)
+    with torch.cuda.stream(stream):
+        return workspace(nbytes, device)
 
 
 def _list(t, n: int, what: str):

@@ -218,12 +218,17 @@ csa2_status check_workspace(const void *ws, size_t ws_bytes, size_t need) {
 
 // The query side of the dense attentions (rows = queries x heads stay far inside 32 bits).
 constexpr int64_t kWindowMaxQueries = 1 << 22;
-csa2_status check_queries(const uint16_t *q, const int32_t *q_pos, const uint16_t *out, int B, int T_q, int H,
-                          int64_t most_queries) {
+csa2_status check_queries(const uint16_t *q, const int32_t *q_pos, const uint16_t *out, int B, int T_q, int H, int D,
+                          const csa2_swa_cache *swa, int64_t most_queries) {
   if (!q || !q_pos || !out || !aligned16(q) || !aligned16(q_pos) || !aligned16(out))
     return fail(CSA2_ERR_INVALID_ARG, "q/q_pos/out must be 16-byte aligned device pointers");
   if (B <= 0 || T_q <= 0 || (int64_t)B * T_q > most_queries) return fail(CSA2_ERR_INVALID_ARG, "B=%d T_q=%d", B, T_q);
   if (H < 1 || H > 64) return fail(CSA2_ERR_UNSUPPORTED_SHAPE, "H=%d not in [1,64]", H);
+  const uintptr_t qa = (uintptr_t)q, oa = (uintptr_t)out, bytes = (uintptr_t)B * T_q * H * D * 2;
+  if (qa < oa + bytes && oa < qa + bytes) return fail(CSA2_ERR_INVALID_ARG, "out overlaps q");
+  if (swa && swa->window > 0 && swa->W_cap < (int64_t)T_q + swa->window - 1)
+    return fail(CSA2_ERR_INVALID_ARG, "W_cap=%d: a chunk of %d tokens needs %lld rows", swa->W_cap, T_q,
+                (long long)T_q + swa->window - 1);
   return CSA2_OK;
 }
 
@@ -741,7 +746,7 @@ csa2_status csa2_prefix_attn_decode(const csa2_page_pool *pool, const int32_t *s
   NvtxRange nvtx("csa2_prefix_attn_decode");
   csa2_status st;
   if ((st = check_pool(pool)) != CSA2_OK) return st;
-  if ((st = check_queries(q, q_pos, out, B, T_q, H, 65535)) != CSA2_OK) return st;
+  if ((st = check_queries(q, q_pos, out, B, T_q, H, pool->D, swa, 65535)) != CSA2_OK) return st;
   if (!seq || !aligned16(seq)) return fail(CSA2_ERR_INVALID_ARG, "seq must be a 16-byte aligned device pointer");
   if (n_shared < 0 || n_shared > (int64_t)pool->max_pages * pool->page)
     return fail(CSA2_ERR_INVALID_ARG, "n_shared=%d outside the table's %d pages", n_shared, pool->max_pages);
@@ -794,10 +799,7 @@ csa2_status csa2_window_attn(const csa2_swa_cache *swa, const csa2_swa_cache *si
     if ((st = check_swa(sinks)) != CSA2_OK) return st;
     if (sinks->B != swa->B || sinks->D != swa->D) return fail(CSA2_ERR_INVALID_ARG, "sinks and window cache disagree");
   }
-  if ((st = check_queries(q, q_pos, out, swa->B, T_q, H, kWindowMaxQueries)) != CSA2_OK) return st;
-  if (swa->window > 0 && swa->W_cap < (int64_t)T_q + swa->window - 1)
-    return fail(CSA2_ERR_INVALID_ARG, "W_cap=%d: a chunk of %d tokens needs %lld rows", swa->W_cap, T_q,
-                (long long)T_q + swa->window - 1);
+  if ((st = check_queries(q, q_pos, out, swa->B, T_q, H, swa->D, swa, kWindowMaxQueries)) != CSA2_OK) return st;
   const int n_sink = sinks ? sinks->window : 0;
   DeviceState *d;
   if ((st = device_state(&d)) != CSA2_OK) return st;

@@ -117,7 +117,8 @@ struct Segment {
   int key0;                // first entry of the first FP4 tile
   int key_lo, key_end;     // entries below and from here on count as zeros
   int seq;                 // pool sequence whose table is read (-1: none)
-  int slot;                // partial result's place, -1: straight to the output
+  size_t ml_at, o_at;      // partial result's (max, sum) and O in the workspace (bytes)
+  int o_rows;              // rows of its planes
   int q0, nq;              // queries of the rows
   int win_lo, win_hi;      // window tokens, where they are one stretch; else win_hi = -1
   int pos[kMaxQ];          // their token positions
@@ -277,23 +278,40 @@ __device__ __forceinline__ int own_tiles(const DenseAttnArgs &a, const Schedule 
   return n > a.n_shared ? (n - s.own0 + kTile - 1) / kTile : 0;
 }
 
-// Workspace: per unit {first slot, slots}, per slot [128] (max, sum), per slot
-// [DO / 4][128] float4 of O.
+// Workspace: per unit {first slot, slots}; per slot of a unit of the prefix (0)
+// or of a sequence's own keys (1) [rows] (max, sum) and [DO / 4][rows] float4 of
+// O, rows = 128 or, where a sequence has fewer, its number.
 struct DenseWs {
-  size_t off_ml, off_o, bytes;
+  size_t off_ml[2], off_o[2], bytes;
+  int rows[2];
 };
-__host__ __device__ __forceinline__ DenseWs dense_ws(long long units, int grid, int DO) {
+__host__ __device__ __forceinline__ DenseWs dense_ws(int rt_sh, long long own_units, int seq_rows, int cs, int grid, int DO) {
   DenseWs w;
-  const long long slots = units + grid;
-  w.off_ml = ((size_t)units * 8 + 255) & ~size_t(255);
-  w.off_o = w.off_ml + (size_t)slots * kRows * 8;
-  w.bytes = w.off_o + (size_t)slots * kRows * DO * 4;
+  w.bytes = ((size_t)cs * (rt_sh + own_units) * 8 + 255) & ~size_t(255);
+  for (int k = 0; k < 2; ++k) {
+    w.rows[k] = k == 0 || seq_rows > kRows ? kRows : seq_rows;
+    const size_t slots = (size_t)(cs * (k == 0 ? rt_sh : own_units) + grid);
+    w.off_ml[k] = w.bytes;
+    w.off_o[k] = w.off_ml[k] + ((slots * w.rows[k] * 8 + 255) & ~size_t(255));
+    w.bytes = w.off_o[k] + ((slots * w.rows[k] * DO * 4 + 255) & ~size_t(255));
+  }
   return w;
 }
+__device__ __forceinline__ DenseWs dense_ws(const DenseAttnArgs &a, const Schedule &sc, int DO) {
+  return dense_ws(sc.rt_sh, (long long)a.B * sc.rt_own, a.T_q * a.H, sc.cs, sc.grid, DO);
+}
+
+// Where the search for the sequence at a linear position was last: the first
+// sequence of a group of 32 and its position within a half's own part.
+struct Cursor {
+  int half, b0;
+  long long at;
+};
 
 // Warp 0: the segment at linear position *x (before x_end); advances *x.
+template <int DO>
 __device__ __forceinline__ bool next_prefix_segment(const DenseAttnArgs &a, const Schedule &sc, long long th, long long chunk,
-                                    long long *x, long long x_end, int lane, Segment &sg) {
+                                    long long *x, long long x_end, int lane, Cursor &cur, Segment &sg) {
 #pragma unroll 1
   while (*x < x_end) {
     const int half = *x >= th ? 1 : 0;   // at most two channel halves
@@ -308,8 +326,9 @@ __device__ __forceinline__ bool next_prefix_segment(const DenseAttnArgs &a, cons
       unit_at = base + rt * one;
     } else {
       y -= sh;
-      long long at = 0;     // linear position of sequence b0 within the own part
-      int b0 = 0, own = 0;
+      if (cur.half != half) cur = Cursor{half, 0, 0};   // (positions only grow)
+      long long at = cur.at;   // linear position of sequence b0 within the own part
+      int b0 = cur.b0, own = 0;
 #pragma unroll 1
       for (;;) {
         const int bb = b0 + lane;
@@ -323,6 +342,8 @@ __device__ __forceinline__ bool next_prefix_segment(const DenseAttnArgs &a, cons
         }
         const uint32_t hit = __ballot_sync(0xffffffffu, at + inc > y);
         if (hit) {
+          cur.b0 = b0;
+          cur.at = at;
           const int l = __ffs(hit) - 1;
           b = b0 + l;
           at += __shfl_sync(0xffffffffu, inc - c, l);
@@ -375,10 +396,17 @@ __device__ __forceinline__ bool next_prefix_segment(const DenseAttnArgs &a, cons
       sg.key_end = shared ? a.n_shared : ents;
       const int u = half * sc.units + unit;
       const int g0 = (int)div64(unit_at + sc.ov, chunk);
-      sg.slot = (int)blockIdx.x + u;
+      // (a unit's parts lie in consecutive blocks, and the next unit starts in
+      // the last one's block or behind it: no two parts meet in a slot)
+      const int u_sort = shared ? half * sc.rt_sh + unit : half * (sc.units - sc.rt_sh) + unit - sc.rt_sh;
+      const DenseWs w = dense_ws(a, sc, DO);
+      const size_t slot = (size_t)((int)blockIdx.x + u_sort);
+      sg.o_rows = shared ? w.rows[0] : w.rows[1];
+      sg.ml_at = (shared ? w.off_ml[0] : w.off_ml[1]) + slot * sg.o_rows * 8;
+      sg.o_at = (shared ? w.off_o[0] : w.off_o[1]) + slot * sg.o_rows * DO * 4;
       if (g0 == (int)blockIdx.x) {
         const long long last = unit_at + sc.ov + (wt > 0 ? nt : nt - 1);
-        reinterpret_cast<int2 *>(a.ws)[u] = make_int2(g0 + u, (int)div64(last, chunk) - g0 + 1);
+        reinterpret_cast<int2 *>(a.ws)[u] = make_int2(g0 + u_sort, (int)div64(last, chunk) - g0 + 1);
       }
     }
     *x = done;
@@ -868,10 +896,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
         }
         fence_proxy_async();   // the next segment's Q lands here
       } else if (MODE == 0 && ok) {
-        const DenseWs w = dense_ws((long long)sc.units * CS, sc.grid, DO);
-        uint8_t *ws = static_cast<uint8_t *>(a.ws);
-        float2 *ml = reinterpret_cast<float2 *>(ws + w.off_ml) + (size_t)sg.slot * kRows;
-        float4 *po = reinterpret_cast<float4 *>(ws + w.off_o) + (size_t)sg.slot * (DO / 4) * kRows;
+        float2 *ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(a.ws) + sg.ml_at);
+        float4 *po = reinterpret_cast<float4 *>(static_cast<uint8_t *>(a.ws) + sg.o_at);
+        const int R = sg.o_rows;
         if (live) ml[row] = make_float2(m_ref, l);
 #pragma unroll 1
         for (int c = 0; c < DO; c += 32) {
@@ -887,7 +914,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
               if (n_tiles > 0)
                 v = make_float4(__uint_as_float(o[4 * j]) * vsc, __uint_as_float(o[4 * j + 1]) * vsc,
                                 __uint_as_float(o[4 * j + 2]) * vsc, __uint_as_float(o[4 * j + 3]) * vsc);
-              po[(size_t)(c / 4 + j) * kRows + row] = v;
+              po[(size_t)(c / 4 + j) * R + row] = v;
             }
           }
         }
@@ -904,6 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
       // ================================================ scheduler: this block's share of the
       // work is [x, x_end) of the tiles' linear order (prefix), every grid-th unit (window)
       long long th = 0, chunk = 1, x, x_end;
+      Cursor cur{-1, 0, 0};
       if (MODE == 0) {
         long long sum = 0;
         for (int b = lane; b < a.B; b += 32) sum += own_length(sc, own_tiles(a, sc, b));
@@ -921,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
         Segment &sg = S.seg[i & 1u];
         bool more;
         if (MODE == 0) {
-          more = next_prefix_segment(a, sc, th, chunk, &x, x_end, lane, sg);
+          more = next_prefix_segment<DO>(a, sc, th, chunk, &x, x_end, lane, cur, sg);
         } else {
           more = x < x_end;
           if (more && lane == 0) {
@@ -930,7 +958,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
             sg.half = half; sg.b = b;
             sg.row0 = b * rows + rt * kRows;
             sg.nrows = rows - rt * kRows < kRows ? rows - rt * kRows : kRows;
-            sg.n_fp4 = 0; sg.key0 = 0; sg.key_lo = 0; sg.key_end = 0; sg.seq = -1; sg.slot = -1;
+            sg.n_fp4 = 0; sg.key0 = 0; sg.key_lo = 0; sg.key_end = 0; sg.seq = -1;
             sg.n_sink = 0;
             sg.n_win = 1;
           }
@@ -1250,18 +1278,19 @@ __global__ void __launch_bounds__(kRows * kMergeShares, 2) attn_dense_merge_kern
   const int ch0 = blockIdx.y * kMergeCh, half = ch0 / DO, c0 = ch0 % DO;
   const int b = live ? (int)(frow / ((long long)a.T_q * a.H)) : 0;
   const int orow = live ? (int)(frow - (long long)b * a.T_q * a.H) : 0;
-  const DenseWs w = dense_ws((long long)sc.units * F::CS, sc.grid, DO);
+  const DenseWs w = dense_ws(a, sc, DO);
   const uint8_t *ws = static_cast<const uint8_t *>(a.ws);
   const int2 *desc = reinterpret_cast<const int2 *>(ws) + (size_t)half * sc.units;
-  const float2 *ml = reinterpret_cast<const float2 *>(ws + w.off_ml);
-  const float4 *po = reinterpret_cast<const float4 *>(ws + w.off_o);
   int2 sh = make_int2(0, 0), ow = make_int2(0, 0);   // (first slot, slots) of the prefix and of the row's own keys
   if (live && sc.nt_sh > 0) sh = __ldcg(desc + blockIdx.x);
   if (live && own_tiles(a, sc, b) + sc.wt > 0) ow = __ldcg(desc + sc.rt_sh + b * sc.rt_own + orow / kRows);
   const int parts = sh.y + ow.y;
-  auto place = [&](int s) -> size_t {   // part s: slot * 128 + row of the slot
-    return s < sh.y ? (size_t)(sh.x + s) * kRows + row : (size_t)(ow.x + s - sh.y) * kRows + orow % kRows;
-  };
+  // this row and channel range in the first part of either sort
+  const int R1 = w.rows[1], r1 = orow % kRows;
+  const float2 *ml0 = reinterpret_cast<const float2 *>(ws + w.off_ml[0]) + (size_t)sh.x * kRows + row;
+  const float2 *ml1 = reinterpret_cast<const float2 *>(ws + w.off_ml[1]) + (size_t)ow.x * R1 + r1;
+  const float4 *po0 = reinterpret_cast<const float4 *>(ws + w.off_o[0]) + ((size_t)sh.x * (DO / 4) + c0 / 4) * kRows + row;
+  const float4 *po1 = reinterpret_cast<const float4 *>(ws + w.off_o[1]) + ((size_t)ow.x * (DO / 4) + c0 / 4) * R1 + r1;
   float M = -INFINITY, L = 0.f;
   float4 acc[kMergeCh / 4];
 #pragma unroll
@@ -1277,11 +1306,11 @@ __global__ void __launch_bounds__(kRows * kMergeShares, 2) attn_dense_merge_kern
 #pragma unroll
       for (int j = 0; j < kMergeCh / 4; ++j) o[u][j] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (s < parts) {
-        const size_t at = place(s);
-        const float4 *p = po + (at / kRows * (DO / 4) + c0 / 4) * kRows + at % kRows;
-        v[u] = __ldcg(&ml[at]);
+        const int k = s < sh.y ? s : s - sh.y, R = s < sh.y ? kRows : R1;
+        const float4 *p = (s < sh.y ? po0 : po1) + (size_t)k * ((DO / 4) * R);
+        v[u] = __ldcg((s < sh.y ? ml0 : ml1) + (size_t)k * R);
 #pragma unroll
-        for (int j = 0; j < kMergeCh / 4; ++j) o[u][j] = __ldcg(p + (size_t)j * kRows);
+        for (int j = 0; j < kMergeCh / 4; ++j) o[u][j] = __ldcg(p + (size_t)j * R);
       }
     }
     float Mn = M;
@@ -1345,12 +1374,6 @@ __global__ void __launch_bounds__(kRows * kMergeShares, 2) attn_dense_merge_kern
 
 namespace {
 
-long long prefix_units(int B, int T_q, int H, int D) {
-  const long long rows = (long long)B * T_q * H;
-  const int cs = D > 256 ? D / 256 : 1;
-  return cs * ((rows + kRows - 1) / kRows + (long long)B * ((T_q * H + kRows - 1) / kRows));
-}
-
 template <int D, int MODE>
 cudaError_t launch_dense(const DenseMaps &m, const DenseAttnArgs &a, const Schedule &sc, cudaStream_t s) {
   const size_t smem = sizeof(DenseSmem<D>) + 1024;
@@ -1382,7 +1405,9 @@ cudaError_t launch_window_t(const DenseMaps &m, const DenseAttnArgs &a, int sms,
 }  // namespace
 
 size_t prefix_attn_workspace_bytes(int B, int T_q, int H, int D, int sms) {
-  return dense_ws(prefix_units(B, T_q, H, D), sms, D < 256 ? D : 256).bytes;
+  const long long rows = (long long)B * T_q * H;
+  const long long own_units = (long long)B * ((T_q * H + kRows - 1) / kRows);
+  return dense_ws((int)((rows + kRows - 1) / kRows), own_units, T_q * H, D > 256 ? D / 256 : 1, sms, D < 256 ? D : 256).bytes;
 }
 cudaError_t launch_prefix_attn(const DenseMaps &m, const DenseAttnArgs &a, int sms, cudaStream_t s) {
   switch (a.D) {

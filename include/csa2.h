@@ -455,9 +455,10 @@ CSA2_API csa2_status csa2_pages_compact(const csa2_page_pool *pool, int32_t *n_l
  *         nothing is shared).  That the sequences agree on them is the
  *         caller's word; a sequence with fewer entries sees only its own
  *         number of them.
- *  swa    window cache of the layer with B rows (NULL: no window)
+ *  swa    window cache of the layer with B rows (NULL: no window); its
+ *         W_cap >= T_q + window - 1, as for the append
  *  q      [B][T_q][H][D] bf16, q_pos [B][T_q] i32 token position t of each query
- *  out    [B][T_q][H][D] bf16: softmax over the entries e < min(n_entries,
+ *  out    [B][T_q][H][D] bf16, not overlapping q: softmax over the entries e < min(n_entries,
  *         floor((t+1)/m)) of the sequence and the window rows of tokens
  *         max(0,t-window+1)..t, of scale * q . x^, FP32 accumulation; zeros
  *         when that set is empty (a padded query: t = -1; t above 2^31 - 4,097 is

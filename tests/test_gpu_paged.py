@@ -458,6 +458,37 @@ def test_prefix_attention(D, H, T, page, n_shared, lens, window):
     run_prefix(D, H, T, page, n_shared, lens, window, seed=D + H + page)
 
 
+@pytest.mark.parametrize("B,H,D,n_shared,window", [(3000, 1, 128, 0, 0), (700, 2, 512, 40, 5), (513, 3, 256, 0, 33)])
+def test_prefix_attention_of_many_short_sequences(B, H, D, n_shared, window):
+    """More sequences than blocks many times over; lengths 0 to 90, sequences
+    listed twice, workspace rows as few as a sequence has."""
+    rng = np.random.default_rng(B)
+    lens = [int(x) for x in (n_shared + rng.integers(0, 90, 40))]
+    pool, seq, values = paged_batch(B, D, 16, n_shared, lens)
+    pick = rng.integers(0, 40, B)
+    pick[0] = 0
+    many = seq[torch.as_tensor(pick, device="cuda")].contiguous()
+    g = gen(B)
+    q = torch.randn(B, 1, H, D, generator=g, device="cuda").to(torch.bfloat16)
+    rows = e4m3_rows(g, B, max(1, window), D)
+    swa = C.SwaCache.of(rows, scale=0.5, window=window) if window else None
+    pos = [[lens[p] + 7 if i % 11 else -1] for i, p in enumerate(pick)]
+    buf, out = guarded((B, 1, H, D))
+    nbytes = C.csa2_prefix_attn_workspace_size(B, 1, H, D)
+    ws = torch.full((nbytes + 4096,), 77, dtype=torch.uint8, device="cuda")
+    C.csa2_prefix_attn_decode(pool, many, n_shared, swa, q, i32(pos), 0.07, out, ws=ws[:nbytes])
+    assert bool((ws[nbytes:] == 77).all()), "wrote behind its workspace"
+    assert bool((buf[:1024] == 7).all()) and bool((buf[-1024:] == 7).all())
+    for b in list(range(0, B, 37)) + [1, 2, B - 1]:
+        t = pos[b][0]
+        keys = [values[pick[b]][: max(0, min(lens[pick[b]], t + 1))]]
+        if window and t >= 0:
+            keys.append(window_keys(rows[b], 0.5, t, window))
+        ref, tol = attend64(q[b, 0].double(), torch.cat(keys), 0.07)
+        check(out[b, 0], ref, tol, f"b {b}")
+    assert C.csa2_device_status() == 0
+
+
 @pytest.mark.parametrize("D,H,T,page,n_shared,lens,window", [
     (128, 8, 1, 16, 300, [340, 301, 517], 128),
     (128, 3, 2, 48, 0, [1, 0, 49, 130], 0),

@@ -8,6 +8,7 @@ import torch
 from fp4_kv_cache_append_b200 import csa2 as C
 
 P = ctypes.c_void_p(16)
+OUT = ctypes.c_void_p(1 << 40)      # behind any q at P
 BIG = 1 << 40
 
 
@@ -70,7 +71,7 @@ def test_attention_refusals():
     L = C.lib()
     odd = ctypes.c_void_p(18)
 
-    def prefix(p=None, seq=P, n_shared=0, w=None, q=P, pos=P, B=2, T=1, H=64, out=P):
+    def prefix(p=None, seq=P, n_shared=0, w=None, q=P, pos=P, B=2, T=1, H=64, out=OUT):
         return L.csa2_prefix_attn_decode(p or pool(), seq, n_shared, w, q, pos, B, T, H, 1.0, out, P, BIG, None)
 
     assert prefix(seq=None) == 1 and prefix(q=odd) == 1 and prefix(pos=None) == 1 and prefix(out=odd) == 1
@@ -79,10 +80,10 @@ def test_attention_refusals():
     assert prefix(H=0) == 2 and prefix(H=65) == 2
     assert prefix(w=swa(B=3)) == 1 and prefix(w=swa(D=256)) == 1 and prefix(w=swa(window=2000, W_cap=4000)) == 1
 
-    def window(w=None, k=None, q=P, T=1, H=64, out=P):
+    def window(w=None, k=None, q=P, T=1, H=64, out=OUT):
         return L.csa2_window_attn(w or swa(), k, q, P, T, H, 1.0, out, P, BIG, None)
 
-    assert L.csa2_window_attn(None, None, P, P, 1, 64, 1.0, P, P, BIG, None) == 1
+    assert L.csa2_window_attn(None, None, P, P, 1, 64, 1.0, OUT, P, BIG, None) == 1
     assert window(w=swa(rows=None)) == 1 and window(w=swa(D=64)) == 2 and window(w=swa(scale=0.0)) == 1
     assert window(T=130) == 1                       # W_cap 256 holds chunks of up to 129 tokens
     assert window(k=swa(B=1)) == 1 and window(k=swa(rows=17)) == 1
@@ -109,3 +110,16 @@ def test_the_binding_checks_shapes():
         C.csa2_prefix_attn_decode(p, one, 0, None, q[..., :64], one.view(1, 1), 1.0, q)
     with pytest.raises(ValueError):
         C.csa2_prefix_attn_decode(p, one, 0, None, q, one.view(1, 1), 1.0, q[:, :, :4])
+
+
+def test_attention_refuses_an_output_over_its_queries_and_a_short_ring():
+    L, last = C.lib(), 16 + 2 * 64 * 512 * 2                # the queries end in front of it
+
+    def prefix(out, w=None, T=1):
+        return L.csa2_prefix_attn_decode(pool(), P, 0, w, P, P, 2, T, 64, 1.0, ctypes.c_void_p(out), P, BIG, None)
+
+    for at in (16, 32, last - 16):
+        assert prefix(at) == 1 and b"overlaps" in L.csa2_last_error()
+        assert L.csa2_window_attn(swa(), None, P, P, 1, 64, 1.0, ctypes.c_void_p(at), P, BIG, None) == 1
+        assert b"overlaps" in L.csa2_last_error()
+    assert prefix(1 << 40, swa(W_cap=128), T=2) == 1 and b"W_cap" in L.csa2_last_error()
