@@ -27,7 +27,7 @@
 //               i + 1 runs during tile i's softmax, O of tile i as soon as its P
 //               is there
 //   warp 15     writes the next segment (see below) while this one runs
-// Q lands as bf16 (its first chunks where the ring will be, the rest in place)
+// Q lands as bf16 (its first chunks in the ring's last groups, the rest in place)
 // and is converted by the softmax and the dequantising warps.  Up to four chunks
 // of Q (256 channels) go to tensor memory as the A operand, the rest stays in
 // shared memory: a K step of 16 with Q in tensor memory takes 33 cycles, with Q
@@ -76,7 +76,8 @@ constexpr int kSmWarp0 = 8;                  // softmax warps 8..11
 constexpr int kMmaWarp = 12;
 constexpr int kTile = 64;                    // keys per tile
 constexpr int kThreads = 16 * 32;            // four warpgroups: registers are split between them
-constexpr int kSegBar = 1, kQBar = 2;        // named barriers: a segment's start and end (all threads); Q in place
+constexpr int kSegBar = 1, kQBar = 2;        // named barriers: a segment's start and end (all threads); Q in place (arrivals
+                                             // of the softmax and dequantising warps, awaited by the issuer of S)
 constexpr int kSchedWarp = 15;               // writes the next segment
 // Registers per thread of the warpgroups: 2 x fetch, softmax, MMA (a tile's
 // logits stay in registers; a spill would go to L2, shared memory takes all of
@@ -132,6 +133,7 @@ struct DenseSmem {
   uint64_t raw_full[kStages], raw_empty[kStages];
   uint64_t full[Cfg<D>::NG];
   uint64_t empty[Cfg<D>::NG];
+  uint64_t q_moved;                                                              // ... and its first chunks are in tensor memory
   uint64_t q_full;                                                               // a segment's Q has landed
   uint64_t s_full[2], p_full[2], pv_done[2], fin;                                // of a tile's buffer
   uint32_t tmem_base;
@@ -162,6 +164,9 @@ __device__ __forceinline__ int load_if(const int32_t *p, bool live, int other) {
 // Asynchronous copies to shared memory; `live` false writes zeros instead.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void named_bar_arrive(int id, int n) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
 // Arrive on `bar` once this thread's copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
@@ -482,6 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
       mbar_init(&S.pv_done[u], 1);
     }
     mbar_init(&S.q_full, 1);
+    mbar_init(&S.q_moved, 4);
     mbar_init(&S.fin, 2);
     S.abort = 0;
     fence_barrier_init();
@@ -498,14 +504,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
 
   bool dead = false;
   // A segment's start: the scheduler warp has written it (or that there is
-  // none).  Its Q in place (not for the scheduler, which writes the next one
-  // meanwhile, and the loader).  Its end: true when a wait of any role gave up.
+  // none).  Its end: true when a wait of any role gave up.
   uint32_t seg_i = 0;
   auto begin_segment = [&]() -> bool {
     named_bar(kSegBar, kThreads);
     return S.more[seg_i & 1u] != 0;
   };
-  auto q_in_place = [&]() { named_bar(kQBar, kThreads - 64); };
+  constexpr int kQBarThreads = kDq + 4 * 32 + 32;
+  // Where chunk k of Q's first ones lands: in the ring's last two groups from
+  // here on, so that the first ones can be filled meanwhile.
+  auto q_staging = [&](uint32_t g0, int k) -> uint8_t * {
+    return S.kv[(g0 + NG - 2 + (uint32_t)(k / (GC / 2))) % NG] + (k % (GC / 2)) * (kRows * 128);
+  };
   auto end_segment = [&]() -> bool {
     ++seg_i;
     return named_bar_or(kSegBar, kThreads, *abort != 0);
@@ -541,10 +551,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
       const int n_sink = sg.n_sink, n_fp4 = sg.n_fp4, n_tiles = n_sink + n_fp4 + sg.n_win;
       const int key0 = sg.key0, key_lo = sg.key_lo, key_end = sg.key_end;
       const int win_lo = sg.win_lo, win_hi = sg.win_hi;
-      // ---- Q's chunks of shared memory: bf16 -> fp16 in place
-      bool ok = all_wait(&S.q_full, seg_i & 1u);
+      // ---- Q's chunks of shared memory: bf16 -> fp16 in place.  Without any (D
+      // 128 and 256) the first groups are filled while Q is on its way: 31.3 us
+      // against 33.1 us (3 x 517 tokens of 20 heads, D 256, window 333)
+      constexpr bool kEarly = QS == 0;
+      bool ok = true;
       if constexpr (QS > 0) {
-        if (ok) {
+        if (all_wait(&S.q_full, seg_i & 1u)) {
 #pragma unroll 4
           for (int i = tid; i < kRows * QS * 8; i += kDq) {
             uint4 *p = reinterpret_cast<uint4 *>(S.q) + i;
@@ -554,7 +567,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
         }
         fence_proxy_async();
       }
-      q_in_place();
+      named_bar_arrive(kQBar, kQBarThreads);
+      if (!kEarly) ok = all_wait(&S.q_moved, seg_i & 1u);
+      const uint32_t g_first = gcount;
       // ---- team t takes the groups whose running number is t modulo 2: the
       // two halves of a tile's channels (D 512), or every other tile.  Lane =
       // (row, 16-byte piece) so that the eight lanes of a load's or a store's
@@ -589,6 +604,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
         if (!mine) continue;
         const uint32_t slot = gi % NG, ph = (gi / NG) & 1u;
         uint8_t *kv = S.kv[slot];
+        // the groups that Q's first chunks landed in
+        if (kEarly && gi - g_first >= NG - 2 && gi - g_first < NG) {
+          ok = all_wait(&S.q_moved, seg_i & 1u);
+          if (!ok) break;
+        }
         if (fp4) {
           const uint32_t st = step % kStages;
           ok = raw_wait(step);
@@ -703,14 +723,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
       const uint32_t lrow = tmem + ((uint32_t)(32 * q) << 16);
       const int frow = sg.row0 + row;
       const bool live = row < sg.nrows;
-      // ---- Q's first chunks, which landed in the ring (no group is in use
-      // yet): this thread's row into its tensor-memory lane.  A rolled loop: at
+      // ---- Q's first chunks, which landed in the ring: this thread's row into its tensor-memory lane.  A rolled loop: at
       // a kernel's start the instructions come from far
       bool ok = all_wait(&S.q_full, seg_i & 1u);
       if (ok) {
-        const uint8_t *qs = S.kv[0] + row * 128;
 #pragma unroll 1
-        for (int k = 0; k < QT; ++k, qs += kRows * 128) {
+        for (int k = 0; k < QT; ++k) {
+          const uint8_t *qs = q_staging(tcount * CS, k) + row * 128;
           uint32_t h[32];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -723,8 +742,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
       }
       tmem_wait_st();
       tc_fence_before();
-      q_in_place();
-      tc_fence_after();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.q_moved);
+      __syncwarp();
+      named_bar_arrive(kQBar, kQBarThreads);
       const int t = live ? sg.pos[frow / a.H - sg.q0] : -1;
       int vis = 0;                                 // entries this row sees
       if (MODE == 0 && t >= 0) {
@@ -1031,8 +1052,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
       const Segment &sg = S.seg[seg_i & 1u];
       const int n_sink = sg.n_sink, n_fp4 = sg.n_fp4, n_tiles = n_sink + n_fp4 + sg.n_win;
       const int half = sg.half;
-      if (warp != kLoadWarp) q_in_place();   // (the loader does not need it)
       if (warp == kMmaWarp) {
+        named_bar(kQBar, kQBarThreads);
         // One elected lane runs the whole loop, its waits included: measured, a
         // converged warp that elects a lane per group of MMAs issues the S
         // product at 59 cycles per MMA even with nothing else on the SM (130 in
@@ -1112,7 +1133,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
           mbar_arrive_expect_tx(&S.q_full, NCH * kRows * 128);
 #pragma unroll 1
           for (int k = 0; k < NCH; ++k)
-            tma_load_2d(k < QT ? S.kv[0] + k * (kRows * 128) : S.q + (k - QT) * (kRows * 128), &q_map, q_chunk(k, half) * 64,
+            tma_load_2d(k < QT ? q_staging(tcount * CS, k) : S.q + (k - QT) * (kRows * 128), &q_map, q_chunk(k, half) * 64,
                         sg.row0, &S.q_full);
         }
         __syncwarp();
@@ -1378,7 +1399,7 @@ template <int D, int MODE>
 cudaError_t launch_dense(const DenseMaps &m, const DenseAttnArgs &a, const Schedule &sc, cudaStream_t s) {
   const size_t smem = sizeof(DenseSmem<D>) + 1024;
   static_assert(sizeof(DenseSmem<D>) + 1024 <= 232448, "shared memory");
-  static_assert(Cfg<D>::QT * kRows <= Cfg<D>::NG * Cfg<D>::GC * kTile, "Q's staging in the ring");
+  static_assert(Cfg<D>::QT * kRows == 2 * Cfg<D>::GC * kTile && Cfg<D>::NG > 2, "Q's staging in the ring");
   static std::atomic<uint64_t> allowed{0};
   const cudaError_t e = allow_smem_once(attn_dense_kernel<D, MODE>, smem, &allowed);
   if (e != cudaSuccess) return e;
