@@ -887,29 +887,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
         // a store lie along a row: a store per lane and row would touch 32 lines
         const float inv = l > 0.f ? vsc / l : 0.f;
 #pragma unroll 1
-        for (int c = 0; c < DO; c += 32) {
-          uint32_t o[32];
+        for (int c = 0; c < DO; c += 64) {
+          uint32_t o[64];
           if (n_tiles > 0) {
             tmem_ld_x32(lrow + kColO + c, o);
+            tmem_ld_x32(lrow + kColO + c + 32, o + 32);
             tmem_wait_ld();
-          }
-          uint32_t pk[16];
+          } else {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float x0 = n_tiles > 0 ? __uint_as_float(o[2 * j]) * inv : 0.f;
-            const float x1 = n_tiles > 0 ? __uint_as_float(o[2 * j + 1]) * inv : 0.f;
-            const __nv_bfloat162 bv = __floats2bfloat162_rn(x0, x1);
-            pk[j] = *reinterpret_cast<const uint32_t *>(&bv);
+            for (int j = 0; j < 64; ++j) o[j] = 0;
           }
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4 *>(S.kv[0] + sw_off(row, c / 8 + j, kRows)) =
-                make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+          for (int j = 0; j < 8; ++j) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const __nv_bfloat162 bv = __floats2bfloat162_rn(__uint_as_float(o[8 * j + 2 * u]) * inv,
+                                                              __uint_as_float(o[8 * j + 2 * u + 1]) * inv);
+              pk[u] = *reinterpret_cast<const uint32_t *>(&bv);
+            }
+            *reinterpret_cast<uint4 *>(S.kv[0] + sw_off(row, c / 8 + j, kRows)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          }
         }
         __syncwarp();   // a warp stores the rows that it has written
         uint16_t *op = a.out + (size_t)sg.row0 * D + half * DO;
         const int nrows = sg.nrows;
-#pragma unroll 4
+#pragma unroll 8
         for (int i = lane; i < 32 * (DO / 8); i += 32) {
           const int r = 32 * q + i / (DO / 8), pc = i % (DO / 8);
           const uint4 v = *reinterpret_cast<const uint4 *>(S.kv[0] + sw_off(r, pc, kRows));
@@ -922,21 +925,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
         const int R = sg.o_rows;
         if (live) ml[row] = make_float2(m_ref, l);
 #pragma unroll 1
-        for (int c = 0; c < DO; c += 32) {
-          uint32_t o[32];
+        for (int c = 0; c < DO; c += 64) {
+          uint32_t o[64];
           if (n_tiles > 0) {
             tmem_ld_x32(lrow + kColO + c, o);
+            tmem_ld_x32(lrow + kColO + c + 32, o + 32);
             tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int j = 0; j < 64; ++j) o[j] = 0;
           }
           if (live) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (n_tiles > 0)
-                v = make_float4(__uint_as_float(o[4 * j]) * vsc, __uint_as_float(o[4 * j + 1]) * vsc,
-                                __uint_as_float(o[4 * j + 2]) * vsc, __uint_as_float(o[4 * j + 3]) * vsc);
-              po[(size_t)(c / 4 + j) * R + row] = v;
-            }
+            for (int j = 0; j < 16; ++j)
+              po[(size_t)(c / 4 + j) * R + row] =
+                  make_float4(__uint_as_float(o[4 * j]) * vsc, __uint_as_float(o[4 * j + 1]) * vsc,
+                              __uint_as_float(o[4 * j + 2]) * vsc, __uint_as_float(o[4 * j + 3]) * vsc);
           }
         }
       }
