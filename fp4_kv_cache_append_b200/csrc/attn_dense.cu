@@ -47,22 +47,22 @@
 // exits.
 //
 // What bounds it (D 512, H 64, 32 sequences of one token, 65,536 shared entries
-// and 512 to 1,024 own ones: 338 us alone, 373 us in a long loop, where the power
-// limit holds the SMs near 1.6 GHz; 747 TFLOP/s of the 4 D FLOP per row and
+// and 512 to 1,024 own ones: 329 us alone, 369 us in a long loop, where the power
+// limit holds the SMs near 1.6 GHz; 755 TFLOP/s of the 4 D FLOP per row and
 // key): shared memory.  A tile of 64 keys and a channel half moves 260 KB through
 // it (S with Q in shared memory 96, in tensor memory 32, O 32, the fp16 keys
 // written 64, the raw bytes in and out 36; the bank counters say the same): 2,030
-// cycles at the 128 bytes a cycle that the S product reaches, of 2,400 measured;
+// cycles at the 128 bytes a cycle that the S product reaches, of 2,350 measured;
 // the tensor core is busy for 1,830 of them.  For D 128 and 256 all of Q is in
 // tensor memory and the softmax's own chain (about 1,650 cycles a tile: 64
 // exponentials on a scheduler's pipe take 512) is the longest: the same case at D
-// 256 takes 138 us (1,010 TFLOP/s), with 32 heads of D 128 74 us.
+// 256 takes 127 us (1,100 TFLOP/s), with 32 heads of D 128 70 us.
 // Loads with a copy instruction per 16 bytes (cp.async) took 2,560 cycles of the
 // loading warp per tile, more than the tile itself: 424 us against 384 us then.
 // A softmax split over two threads per row halves its arithmetic but has them
 // exchange maxima through shared memory in every tile: 440 us against 384 us
 // then, and at D 256, where no S operand of Q is read beside it, 193 us against
-// 138 us.
+// 138 us then.
 #include "attn_dense.cuh"
 #include "kernels_paged.h"
 

@@ -688,9 +688,9 @@ static cudaError_t launch_t(const CUtensorMap &q_map, const DenseAttnArgs &a, in
 // has two blocks for a tile of D 512 and starts sooner, is ahead, unless its
 // second block makes a second wave or all keys are one tile of its own.  us,
 // resident | other, one token of H heads, window 128 and 4 sinks: B 16 H 64 D 512
-// 16.2 | 14.6, B 74 17.0 | 16.0, B 148 19.1 | 28.5; H 16 D 256 B 64 14.1 | 12.8,
-// B 600 54.7 | 50.9 (window of 16: 34.4 | 40.3); H 64 D 128 B 148 13.2 | 10.8,
-// B 1,000 65.8 | 56.3.  Chunks of tokens: 8 x 8, H 64 D 512 16.6 | 17.3; 64 x 4
+// 16.2 | 14.6, B 74 17.0 | 15.9, B 148 19.1 | 28.5; H 16 D 256 B 64 14.1 | 12.8,
+// B 600 54.7 | 45.7 (window of 16: 34.4 | 40.3); H 64 D 128 B 148 13.2 | 10.8,
+// B 1,000 65.8 | 53.9.  Chunks of tokens: 8 x 8, H 64 D 512 16.6 | 17.3; 64 x 4
 // 18.7 | 32.4; 1 x 8,192 234 | 786; H 8 D 128 34.3 | 36.4.
 bool window_takes_ring(const DenseAttnArgs &a, int sms) {
   const int keys = a.n_sink + (a.window > 0 ? a.window + tile_queries(a) - 1 : 0);
