@@ -623,7 +623,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
               rv[u][y] = *reinterpret_cast<const uint4 *>(S.raw[st] + raw_off<F::CB>(r0 + 8 * y, p4 + 4 * u));
               sb[u][y] = *reinterpret_cast<const uint16_t *>(S.raw[st] + kRawSc + (r0 + 8 * y) * F::SB + (p4 + 4 * u) * 2);
             }
-          __syncwarp();                                    // this warp's part of the stage is in registers
+          // this warp's part of the stage is in registers.  (The fence: an arrival
+          // overtakes loads that wait for shared memory beside the S product, and
+          // a tensor copy would then write what they have yet to read.)
+          fence_proxy_async();
+          __syncwarp();
           if (lane == 0) mbar_arrive(&S.raw_empty[st]);
           const int k0 = key0 + (it - n_sink) * kTile;
           if (k0 < key_lo || k0 + kTile > key_end) {   // what the copies brought of other entries: zeros
@@ -678,6 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
 #pragma unroll
               for (int y = 0; y < 2; ++y)
                 rv[u][y] = *reinterpret_cast<const uint4 *>(S.raw[st] + raw_off<kRawRow>(r0 + 8 * y, p4 + 4 * u));
+            fence_proxy_async();   // (as above)
             __syncwarp();
             if (lane == 0) mbar_arrive(&S.raw_empty[st]);
             if (keys < kTile) {

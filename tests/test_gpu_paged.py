@@ -501,6 +501,27 @@ def test_prefix_attention_among_bytes_of_nan(D, H, T, page, n_shared, lens, wind
     run_prefix(D, H, T, page, n_shared, lens, window, seed=D + H, poison=True)
 
 
+def test_prefix_attention_gives_the_same_bits_in_every_launch():
+    """Every one of a thousand launches is compared: a copy that overtakes the
+    loads of the stage it overwrites shows in a few of a hundred (and by too
+    little for the tolerances of the other tests)."""
+    B, H, D, n_shared = 8, 64, 512, 4097
+    g = gen(41)
+    pool, seq, _ = paged_batch(5, D, 128, n_shared, [n_shared + 500 - 30 * b for b in range(B)])
+    swa = C.SwaCache.of(e4m3_rows(g, B, 128, D), scale=1.0, window=128)
+    q = torch.randn(B, 1, H, D, generator=g, device="cuda").to(torch.bfloat16)
+    pos = i32([[n_shared + 499 - 30 * b] for b in range(B)])
+    ws = C.workspace(C.csa2_prefix_attn_workspace_size(B, 1, H, D))
+    first = torch.empty_like(q)
+    C.csa2_prefix_attn_decode(pool, seq, n_shared, swa, q, pos, 0.044, first, ws=ws)
+    outs = torch.empty(50, *q.shape, dtype=q.dtype, device="cuda")
+    for _ in range(20):
+        for o in outs:
+            C.csa2_prefix_attn_decode(pool, seq, n_shared, swa, q, pos, 0.044, o, ws=ws)
+        assert not bool((outs != first).any())
+    assert C.csa2_device_status() == 0
+
+
 @pytest.mark.parametrize("form", ["prefix 512", "prefix 128", "window 256 of 333", "window 512 of 128"])
 def test_attention_launched_back_to_back_gives_the_same_bits(form):
     """Thousands of launches that overlap at their ends: the stages that the
