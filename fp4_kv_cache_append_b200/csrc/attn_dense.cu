@@ -47,7 +47,7 @@
 // exits.
 //
 // What bounds it (D 512, H 64, 32 sequences of one token, 65,536 shared entries
-// and 512 to 1,024 own ones: 329 us alone, 369 us in a long loop, where the power
+// and 512 to 1,024 own ones: 334 us alone, 367 us in a long loop, where the power
 // limit holds the SMs near 1.6 GHz; 755 TFLOP/s of the 4 D FLOP per row and
 // key): shared memory.  A tile of 64 keys and a channel half moves 260 KB through
 // it (S with Q in shared memory 96, in tensor memory 32, O 32, the fp16 keys
