@@ -776,6 +776,42 @@ def test_prompt_forked_into_samples_that_decode():
     assert C.csa2_device_status() == 0
 
 
+def test_calls_on_several_streams_at_once():
+    """Persistent blocks of different launches, their tensor memory and shared
+    memory side by side; each call with a workspace of its own."""
+    g, D = gen(51), 256
+    calls, outs = [], []
+    for k, (n_shared, H) in enumerate(((900, 32), (0, 8))):
+        pool, seq, _ = paged_batch(60 + k, D, 32, n_shared, [n_shared + 300, n_shared + 41, n_shared + 90])
+        q = torch.randn(3, 1, H, D, generator=g, device="cuda").to(torch.bfloat16)
+        pos, ws, out = i32([[2000]] * 3), C.workspace(C.csa2_prefix_attn_workspace_size(3, 1, H, D)), torch.empty_like(q)
+        calls.append(lambda p=pool, s=seq, n=n_shared, q=q, t=pos, o=out, w=ws:
+                     C.csa2_prefix_attn_decode(p, s, n, None, q, t, 0.06, o, ws=w))
+        outs.append(out)
+    for W, T in ((100, 40), (400, 40), (64, 1)):
+        swa = C.SwaCache.of(e4m3_rows(g, 4, W + T, D), scale=0.5, window=W)
+        q = torch.randn(4, T, 16, D, generator=g, device="cuda").to(torch.bfloat16)
+        pos, out = i32([[700 + j for j in range(T)]] * 4), torch.empty_like(q)
+        calls.append(lambda s=swa, q=q, t=pos, o=out: C.csa2_window_attn(s, None, q, t, 0.06, o))
+        outs.append(out)
+    for call in calls:
+        call()
+    ref = [o.clone() for o in outs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(10):
+        for o in outs:
+            o.fill_(7)
+        torch.cuda.synchronize()
+        for _ in range(30):
+            for stream, call in zip(streams, calls):
+                with torch.cuda.stream(stream):
+                    call()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, r) for o, r in zip(outs, ref))
+    assert C.csa2_device_status() == 0
+
+
 def test_on_a_side_stream_and_in_a_replayed_graph():
     D, H, B = 256, 16, 3
     pool, seq, values = paged_batch(31, D, 32, 200, [230, 201, 260])
