@@ -334,7 +334,15 @@ cudaError_t launch_page_append(const PageAppendArgs &a, void *ws, int sms, cudaS
 
 // Every child's new row is taken (and its pages' counts raised) before any row
 // is overwritten, so that a sequence can be a parent and a child in one call.
-//
+
+// Whether pair j sets child c: a pair whose parent is out of range does not use
+// up its child.
+__device__ __forceinline__ bool pair_sets(const PageForkArgs &a, int j, int c) {
+  if (a.child[j] != c) return false;
+  const int p = a.parent[j];
+  return p >= -1 && p < a.pool.n_seq;
+}
+
 // Short lists: one cluster, pair i in block i % 8, with a cluster barrier between
 // the two halves and the taken rows in registers.  One launch instead of two:
 // 6.9 us a call instead of 9.8 (8 sequences of 40 pages, back to back: what the
@@ -350,7 +358,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_fork_kernel(const PageForkA
   if (i < a.n) {
     const int p = a.parent[i], c = a.child[i];
     bool bad = p < -1 || p >= P.n_seq || c < 0 || c >= P.n_seq;
-    for (int j = lane; j < i; j += 32) bad |= a.child[j] == c;
+    for (int j = lane; j < i; j += 32) bad |= pair_sets(a, j, c);
     bad = __any_sync(0xffffffffu, bad);
     if (lane == 0) {
       if (bad) flag(P.status, CSA2_DEV_BAD_SEQUENCE);
@@ -393,7 +401,7 @@ __global__ void __launch_bounds__(kCopyThreads) page_fork_take_kernel(const Page
   pdl_wait();
   const int p = a.parent[i], c = a.child[i];
   bool dup = false;
-  for (int j = tid; j < i; j += kCopyThreads) dup |= a.child[j] == c;
+  for (int j = tid; j < i; j += kCopyThreads) dup |= pair_sets(a, j, c);
   const bool bad = __syncthreads_or(dup) || p < -1 || p >= P.n_seq || c < 0 || c >= P.n_seq;
   if (tid == 0) {
     if (bad) flag(P.status, CSA2_DEV_BAD_SEQUENCE);

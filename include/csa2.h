@@ -428,8 +428,8 @@ CSA2_API size_t csa2_pages_workspace_size(const csa2_page_pool *pool, int n);
  *    its pages (no entry moves); what child[i] held is released.  parent[i] =
  *    -1 empties child[i].  All parents are taken as they stand when the call
  *    starts, so one call can permute or replace sequences (a beam step).  A
- *    child listed twice is set once, by its first listing
- *    (CSA2_DEV_BAD_SEQUENCE).
+ *    child listed twice is set once, by its first pair whose parent is in
+ *    range; every other pair of it is skipped (CSA2_DEV_BAD_SEQUENCE).
  *  parent, child [n] i32 DEVICE; ws: csa2_pages_workspace_size(pool, n) bytes
  * Supported: 1 <= n <= 4096.
  */
