@@ -494,7 +494,10 @@ __global__ void __launch_bounds__(kPlanThreads) page_compact_plan_kernel(const P
     __syncthreads();
   }
   if (tid == 0) {
-    head[0] = lives;
+    // as many of the one as of the other, unless a count is negative (such a
+    // page is neither): only what has both ends moves
+    if (lives != holes) flag(P.status, CSA2_DEV_INDEX_RANGE);
+    head[0] = lives < holes ? lives : holes;
     head[1] = L;
     if (n_live) *n_live = L;
   }
@@ -547,7 +550,7 @@ __global__ void __launch_bounds__(kCopyThreads) page_compact_move_kernel(const P
       else hi = mid;
     }
     if (from[lo] == pg) P.table[x] = to[lo];
-    else flag(P.status, CSA2_DEV_INDEX_RANGE);   // a slot that holds a page without references
+    else flag(P.status, CSA2_DEV_INDEX_RANGE);   // a slot that holds a page without references (or one that could not move)
   }
 }
 

@@ -439,7 +439,9 @@ CSA2_API csa2_status csa2_pages_fork(const csa2_page_pool *pool, const int32_t *
 /*
  * 9. Compact: with L pages in use, those at L and above move into the free
  *    ones below L (the k-th of the one to the k-th of the other) and every
- *    table follows, so that pages L .. n_pages - 1 are free.
+ *    table follows, so that pages L .. n_pages - 1 are free.  (A negative
+ *    count, which no call makes, is neither: pages that then find no free one
+ *    below L stay, CSA2_DEV_INDEX_RANGE.)
  *  n_live i32 DEVICE out (may be NULL): L
  *  ws: csa2_pages_workspace_size(pool, 1) bytes
  */

@@ -41,3 +41,33 @@ def test_fork_by_a_refused_parent_leaves_the_child_to_the_next_pair(n, M):
     assert ref.n_entries[child[0]] == 16 * lens[1]
     ref.same(pool)
     assert C.csa2_device_status() == C.DEV_BAD_SEQUENCE
+
+
+@pytest.mark.parametrize("n_pages,bad", [(20, [0]), (20, [1, 3, 5]), (6000, [7, 4000, 4500])])
+def test_compact_moves_nothing_without_a_free_page(n_pages, bad):
+    """Negative counts (a pool that was never well formed) leave fewer holes
+    below the boundary than pages above it; what has no place stays."""
+    pool = C.PagePool(n_pages, 16, 2, n_pages, 128)
+    pool.codes.copy_((torch.arange(n_pages, device="cuda") % 251).view(-1, 1, 1).expand_as(pool.codes))
+    refs = np.zeros(n_pages, np.int32)
+    refs[[2, 4]], refs[n_pages // 2:], refs[bad] = 1, 1, -1
+    live = np.flatnonzero(refs > 0)
+    table = np.full((2, n_pages), -1, np.int32)
+    table[0, : live.size] = live
+    pool.refs, pool.table = i32(refs), i32(table)
+    pool.n_entries = i32([16 * live.size, 0])
+    L = live.size
+    src, dst = live[live >= L], np.array([p for p in range(L) if refs[p] == 0])
+    k = min(src.size, dst.size)
+    assert dst.size < src.size
+    to = np.arange(n_pages)
+    to[src[:k]] = dst[:k]
+    n_live = torch.zeros(1, dtype=torch.int32, device="cuda")
+    C.csa2_pages_compact(pool, n_live)
+    assert int(n_live) == L and C.csa2_device_status() == C.DEV_INDEX_RANGE
+    assert np.array_equal(pool.table.cpu().numpy()[0, : live.size], to[live])
+    want = refs.copy()
+    want[dst[:k]], want[src[:k]] = refs[src[:k]], 0
+    assert np.array_equal(pool.refs.cpu().numpy(), want)
+    got = pool.codes[torch.as_tensor(to[live], device="cuda")][:, 0, 0].cpu().numpy()
+    assert np.array_equal(got, live % 251)
