@@ -20,9 +20,10 @@
 //               warps take the groups in turn.  The chunks that only S needs
 //               come first and are freed first
 //   warps 8-11  softmax, one row per thread: no exchange between threads.  The
-//               reference maximum moves only when a logit exceeds it by 2^15;
-//               O is then rescaled in tensor memory.  P goes back to tensor
-//               memory (fp16) as the A operand of the second product
+//               reference maximum moves only when a weight exceeds its by 2^6.9;
+//               O is then rescaled in tensor memory.  P, 2^9 times the weight
+//               against the reference, goes back to tensor memory (fp16) as the
+//               A operand of the second product
 //   warps 12, 14  tcgen05.mma issuers of S and of O, one lane each: S of tile
 //               i + 1 runs during tile i's softmax, O of tile i as soon as its P
 //               is there
@@ -92,7 +93,15 @@ constexpr int kRawRow = 128, kRawSc = kTile * kRawRow, kRawBytes = kRawSc + kTil
 // A unit's start and end in tiles (see Schedule::ov): the case above takes 427 us
 // with 2, 363 with 5, 343 with 8, 345 with 10 and 349 with 16.
 constexpr int kUnitCost = 8;
-constexpr float kLazy = 15.0f;               // log2 headroom of P below fp16's 65,504
+// P = 2^(x - reference + kBias), at most 2^(kBias + kLazy) = 61,147, below fp16's
+// 65,504.  The row's largest weight is then at least 2^9, weights down to 2^-23
+// of it keep fp16's 11 bits and none above 2^-34 of it becomes 0, while the
+// denominator sums all of them in fp32: n keys lose at most n 2^-34 of the row's
+// weight.  (Without the bias n 2^-25: one key 17 nats above a million equal ones
+// took 3% from the output.)  A lower limit moves the reference more often: a
+// window of 333 at D 256 takes 30.6 us with limits of 15 and 6.9, 30.8 with 7
+// and a bias of 8, 31.2 with 5.9 and 10.
+constexpr float kBias = 9.0f, kLazy = 6.9f;
 // TMEM columns: O, S of two tiles (each later its P), Q's first chunks
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 384, kTmemCols = 512;
 
@@ -842,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
         const float mu = m_ref == -INFINITY ? 0.f : m_ref;
         uint32_t pr[kTile / 2];
         {
-          const uint64_t l2 = f32x2(lsc, lsc), m2 = f32x2(-mu, -mu);
+          const uint64_t l2 = f32x2(lsc, lsc), m2 = f32x2(kBias - mu, kBias - mu);
           uint64_t ls0 = 0, ls1 = 0;
 #pragma unroll
           for (int j = 0; j < kTile / 2; ++j) {

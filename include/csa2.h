@@ -466,7 +466,9 @@ CSA2_API csa2_status csa2_pages_compact(const csa2_page_pool *pool, int32_t *n_l
  *         when that set is empty (a padded query: t = -1; t above 2^31 - 4,097 is
  *         taken as -1, CSA2_DEV_BAD_POSITION)
  *  ws, ws_bytes: csa2_prefix_attn_workspace_size(B, T_q, H, D) bytes
- * |q| must be below 65,504 (the products run in fp16).
+ * |q| must be below 65,504 (the products run in fp16).  Weights are rounded to
+ * fp16 for the second product, the largest of a row lying at 2^9 or above: n
+ * keys lose at most n 2^-34 of a row's weight.
  * Supported: 1 <= H <= 64, B * T_q <= 65,535, window <= 1024.
  */
 CSA2_API csa2_status csa2_prefix_attn_decode(const csa2_page_pool *pool, const int32_t *seq, int n_shared,

@@ -71,3 +71,70 @@ def test_compact_moves_nothing_without_a_free_page(n_pages, bad):
     assert np.array_equal(pool.refs.cpu().numpy(), want)
     got = pool.codes[torch.as_tensor(to[live], device="cuda")][:, 0, 0].cpu().numpy()
     assert np.array_equal(got, live % 251)
+
+
+# --------------------------------------------------------------------------- weights far below the largest
+
+
+def attend64_tail(q, keys, scale):
+    """attend64, but for weights that fp16 flushes.  The dense kernels hold the
+    row's largest weight at 2^9 or above, so half of fp16's smallest step, 2^-25,
+    is 2^-34 of it: n keys lose n 2^-34 max|v| / (sum of weights) at most."""
+    out, _ = attend64(q, keys, scale)
+    D, n = q.shape[1], keys.shape[0]
+    x = q @ keys.T * scale
+    w = torch.exp(x - x.amax(1, keepdim=True))
+    tot = w.sum(1, keepdim=True)
+    mag = (q.abs() @ keys.abs().T * abs(scale)).amax(1, keepdim=True)
+    rel = 2.0 ** -11 + 2 * (D * 2.0 ** -23 * mag + 2.0 ** -20 * x.abs().amax(1, keepdim=True)) + n * 2.0 ** -23 \
+        + 3 * 2.0 ** -20
+    return out, 2.0 ** -8 * out.abs() + rel * (w @ keys.abs() / tot) + n * 2.0 ** -34 * keys.abs().amax() / tot
+
+
+def levels(H, D):
+    """Queries [H][D] whose product with sixteen ones in front is 10 to 31 bits."""
+    q = torch.zeros(H, D, dtype=torch.float64, device="cuda")
+    q[:, :16] = (torch.linspace(10, 31, H, dtype=torch.float64, device="cuda") * math.log(2) / 16).unsqueeze(1)
+    return q.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("D,B,n,shared", [(128, 300, 4096, True), (256, 300, 3000, True), (512, 150, 4096, True),
+                                          (512, 160, 1500, False), (128, 300, 1500, False)])
+def test_prefix_attention_keeps_the_tail_under_one_dominant_key(D, B, n, shared):
+    """Entry 0 alone has the query's channels, the others alone the rest, where
+    the output is their total weight.  As many row tiles as SMs: no cut in the keys."""
+    H, page, g = 64, 64, gen(D + n)
+    n_pages = -(-n // page)
+    pool = C.PagePool(n_pages, page, 1, n_pages, D)
+    codes = torch.randint(0x11, 0x78, (n_pages * page, D // 2), generator=g, device="cuda", dtype=torch.uint8) & 0x77
+    codes[:, :8] = 0
+    codes[0] = 0
+    codes[0, :8] = 0x22                                  # sixteen ones
+    scales = torch.full((n_pages * page, D // 16), 0x38, dtype=torch.uint8, device="cuda")
+    pool.codes, pool.scales = codes.view(n_pages, page, -1), scales.view(n_pages, page, -1)
+    pool.table, pool.refs, pool.n_entries = i32(range(n_pages)).view(1, -1), i32([1] * n_pages), i32([n])
+    q = levels(H, D).expand(B, 1, H, D).contiguous()
+    out = torch.empty_like(q)
+    C.csa2_prefix_attn_decode(pool, i32([0] * B), n if shared else 0, None, q, i32([[n - 1]] * B), 1.0, out)
+    grid = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64, device="cuda")
+    keys = grid[torch.stack([codes & 15, codes >> 4], -1).flatten(-2).long()][:n]
+    ref, tol = attend64_tail(q[0, 0].double(), keys, 1.0)
+    for b in range(B):
+        check(out[b, 0], ref, tol, f"b {b}")
+    assert C.csa2_device_status() == 0
+
+
+@pytest.mark.parametrize("D,W", [(128, 1024), (256, 700), (512, 1024), (512, 128)])
+def test_window_attention_keeps_the_tail_under_one_dominant_key(D, W):
+    H, g = 64, gen(D)
+    rows = torch.rand(2, W, D, generator=g, device="cuda") + 0.5
+    rows[:, :, :16] = 0
+    rows[:, 0] = 0
+    rows[:, 0, :16] = 1                                  # the window's first token
+    rows = rows.to(torch.float8_e4m3fn)
+    q = levels(H, D).expand(2, 1, H, D).contiguous()
+    out = torch.empty_like(q)
+    C.csa2_window_attn(C.SwaCache.of(rows.view(torch.uint8), scale=1.0, window=W), None, q, i32([[W - 1]] * 2), 1.0, out)
+    for b in range(2):
+        check(out[b, 0], *attend64_tail(q[b, 0].double(), rows[b].double(), 1.0), f"b {b}")
+    assert C.csa2_device_status() == 0
