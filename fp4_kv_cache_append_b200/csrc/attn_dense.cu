@@ -29,7 +29,13 @@
 //               is there
 //   warp 15     writes the next segment (see below) while this one runs
 // Q lands as bf16 (its first chunks in the ring's last groups, the rest in place)
-// and is converted by the softmax and the dequantising warps.  Up to four chunks
+// and is converted by the softmax and the dequantising warps to fp16, each row
+// times a power of two that the logits' factor takes back: 2^6 where the row's
+// largest element lies in [2^-8, 2^9), else the one that brings it to [2^14,
+// 2^15), so that rounding moves an element by 2^-23 of the row's largest at most.
+// That one is found in the same pass; rows that need another power are converted
+// a second time.  (A single token's 15.2 us at D 512 without any of it, 15.7 so,
+// 16.1 with the largest found in a pass of its own.)  Up to four chunks
 // of Q (256 channels) go to tensor memory as the A operand, the rest stays in
 // shared memory: a K step of 16 with Q in tensor memory takes 33 cycles, with Q
 // in shared memory 49 (128 rows of A and 64 of B are read), and the room it
@@ -77,8 +83,10 @@ constexpr int kSmWarp0 = 8;                  // softmax warps 8..11
 constexpr int kMmaWarp = 12;
 constexpr int kTile = 64;                    // keys per tile
 constexpr int kThreads = 16 * 32;            // four warpgroups: registers are split between them
-constexpr int kSegBar = 1, kQBar = 2;        // named barriers: a segment's start and end (all threads); Q in place (arrivals
-                                             // of the softmax and dequantising warps, awaited by the issuer of S)
+// Named barriers: a segment's start and end (all threads); Q in place (arrivals of
+// the softmax and dequantising warps, awaited by the issuer of S); the largest
+// elements of Q's rows (of the softmax and dequantising warps).
+constexpr int kSegBar = 1, kQBar = 2, kQTopBar = 3;
 constexpr int kSchedWarp = 15;               // writes the next segment
 // Registers per thread of the warpgroups: 2 x fetch, softmax, MMA (a tile's
 // logits stay in registers; a spill would go to L2, shared memory takes all of
@@ -147,6 +155,7 @@ struct DenseSmem {
   uint64_t s_full[2], p_full[2], pv_done[2], fin;                                // of a tile's buffer
   uint32_t tmem_base;
   int abort;
+  uint32_t qtop[3][kRows];                                                       // largest magnitudes (row_pow) of Q's first chunks and of the rest's halves
   int more[2];
   Segment seg[2];                                                                // this one and the next
 };
@@ -184,6 +193,19 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void mbar_arrive_n(uint64_t *bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
+
+// Power of two that a row of Q is multiplied by, as fp32's exponent field; `top2`:
+// the largest magnitudes of its even and odd channels as bits of bf16.
+constexpr uint32_t kQPow = 127 + 6;
+__device__ __forceinline__ uint32_t row_pow(uint32_t top2) {
+  const uint32_t top = top2 >> 16 > (top2 & 0xFFFFu) ? top2 >> 16 : top2 & 0xFFFFu, e = top >> 7;
+  if (top == 0 || (e >= 127 - 8 && e < 127 + 9)) return kQPow;
+  return e < 15u ? 253u : 268u - e;   // (2^126 at most)
+}
+__device__ __forceinline__ uint32_t top_of(uint32_t top2, uint4 v) {
+  top2 = __vimax3_u16x2(top2, v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu);
+  return __vimax3_u16x2(top2, v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu);
 }
 
 // The next stretch of at most 64 window tokens at or behind `cur` that the
@@ -532,12 +554,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
   // Chunk of Q (64 channels) that S takes k-th: the other half's channels
   // first.
   auto q_chunk = [&](int k, int half) -> int { return CS > 1 ? (k + (half == 0 ? GC : 0)) % NCH : k; };
-  // bf16 -> fp16 with the sign of the softmax scale (so that the logits' own
-  // factor is not negative).
-  const float qsign = a.scale < 0.f ? -1.f : 1.f;
-  auto to_f16x2 = [&](uint32_t w) -> uint32_t {
-    const __half2 hv = __floats2half2_rn(bf16_to_f32(w & 0xFFFFu) * qsign, bf16_to_f32(w >> 16) * qsign);
+  // bf16 -> fp16 times the row's power of two, with the sign of the softmax scale
+  // (so that the logits' own factor is not negative).
+  auto q_factor = [&](uint32_t field) -> float { return __uint_as_float((field << 23) | (a.scale < 0.f ? 0x80000000u : 0u)); };
+  auto to_f16x2 = [&](uint32_t w, float pow) -> uint32_t {
+    const __half2 hv = __floats2half2_rn(bf16_to_f32(w & 0xFFFFu) * pow, bf16_to_f32(w >> 16) * pow);
     return *reinterpret_cast<const uint32_t *>(&hv);
+  };
+  auto to_f16x4 = [&](uint4 v, float pow) -> uint4 {   // (8 elements)
+    return make_uint4(to_f16x2(v.x, pow), to_f16x2(v.y, pow), to_f16x2(v.z, pow), to_f16x2(v.w, pow));
   };
   // A converged warp's wait, polled by all its lanes: one that lane 0 polls for
   // the others leaves it behind at times, and the tcgen05 instructions that
@@ -566,13 +591,42 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
       constexpr bool kEarly = QS == 0;
       bool ok = true;
       if constexpr (QS > 0) {
-        if (all_wait(&S.q_full, seg_i & 1u)) {
-#pragma unroll 4
-          for (int i = tid; i < kRows * QS * 8; i += kDq) {
-            uint4 *p = reinterpret_cast<uint4 *>(S.q) + i;
-            const uint4 v = *p;
-            *p = make_uint4(to_f16x2(v.x), to_f16x2(v.y), to_f16x2(v.z), to_f16x2(v.w));
+        // (thread = a row's share of the chunks)
+        static_assert(kDq == 2 * kRows && QS % 2 == 0, "a row's chunks in two shares");
+        constexpr int SH = QS / 2;
+        const int row = tid % kRows, part = tid / kRows;
+        auto piece = [&](int k, int i) {
+          return reinterpret_cast<uint4 *>(S.q + (part * SH + k) * (kRows * 128) + row * 128 + ((i ^ (row & 7)) << 4));
+        };
+        const bool landed = all_wait(&S.q_full, seg_i & 1u);
+        uint32_t top2 = 0;
+        if (landed) {
+          const float pow = q_factor(kQPow);
+#pragma unroll 1
+          for (int k = 0; k < SH; ++k) {
+#pragma unroll
+            for (int h = 0; h < 8; h += 4) {
+              uint4 v[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) v[i] = *piece(k, h + i);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                top2 = top_of(top2, v[i]);
+                *piece(k, h + i) = to_f16x4(v[i], pow);
+              }
+            }
           }
+        }
+        S.qtop[1 + part][row] = top2;
+        named_bar(kQTopBar, kDq + 4 * 32);
+        const uint32_t qf = row_pow(__vimax3_u16x2(S.qtop[0][row], S.qtop[1][row], S.qtop[2][row]));
+        if (landed && qf != kQPow) {   // once more, from memory (rows behind the last are zeros: not here)
+          const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (size_t)(sg.row0 + row) * D);
+#pragma unroll 1
+          for (int k = 0; k < SH; ++k)
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i)
+              *piece(k, i) = to_f16x4(__ldg(src + q_chunk(QT + part * SH + k, sg.half) * 8 + i), q_factor(qf));
         }
         fence_proxy_async();
       }
@@ -740,7 +794,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
       // ---- Q's first chunks, which landed in the ring: this thread's row into its tensor-memory lane.  A rolled loop: at
       // a kernel's start the instructions come from far
       bool ok = all_wait(&S.q_full, seg_i & 1u);
-      if (ok) {
+      uint32_t top2 = 0;
+      auto move_q = [&](float pow) {
 #pragma unroll 1
         for (int k = 0; k < QT; ++k) {
           const uint8_t *qs = q_staging(tcount * CS, k) + row * 128;
@@ -748,11 +803,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const uint4 v = *reinterpret_cast<const uint4 *>(qs + ((i ^ (row & 7)) << 4));
-            h[4 * i] = to_f16x2(v.x); h[4 * i + 1] = to_f16x2(v.y);
-            h[4 * i + 2] = to_f16x2(v.z); h[4 * i + 3] = to_f16x2(v.w);
+            top2 = top_of(top2, v);
+            h[4 * i] = to_f16x2(v.x, pow); h[4 * i + 1] = to_f16x2(v.y, pow);
+            h[4 * i + 2] = to_f16x2(v.z, pow); h[4 * i + 3] = to_f16x2(v.w, pow);
           }
           tmem_st_x32(lrow + kColQ + 32 * k, h);
         }
+      };
+      float qpow = q_factor(kQPow), unpow = __uint_as_float((254u - kQPow) << 23);
+#pragma unroll 1
+      for (int turn = 0; turn < 2; ++turn) {   // twice where a row of the warp needs another power
+        if (ok) move_q(qpow);
+        if (turn > 0) break;
+        if constexpr (QS > 0) {
+          S.qtop[0][row] = top2;
+          named_bar(kQTopBar, kDq + 4 * 32);
+          top2 = __vimax3_u16x2(top2, S.qtop[1][row], S.qtop[2][row]);
+        }
+        const uint32_t qf = row_pow(top2);
+        const bool same = __all_sync(0xffffffffu, qf == kQPow) != 0;
+        __syncwarp();
+        if (same) break;
+        qpow = q_factor(qf);
+        unpow = __uint_as_float((254u - qf) << 23);
+        tmem_wait_st();
       }
       tmem_wait_st();
       tc_fence_before();
@@ -812,7 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
         if (!ok) break;
         tc_fence_after();
         // logits in base 2: lsc x S; never 0, so that a hidden key's -inf stays
-        const float lsc = fmaxf(fabsf(a.scale) * ksc * kLog2e, 1e-30f);
+        const float lsc = fmaxf(fabsf(a.scale) * ksc * kLog2e * unpow, 1e-30f);
         uint32_t sv[kTile];
         tmem_ld_x32(scol, sv);
         tmem_ld_x32(scol + 32, sv + 32);

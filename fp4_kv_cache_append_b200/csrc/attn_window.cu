@@ -241,8 +241,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
     const uint32_t lrow = tmem + ((uint32_t)(32 * q) << 16);
     // y = log2(weight x key scale) = S x l + o, with the sign of the softmax
     // scale taken into S and the factor never 0, so that a hidden key's -inf stays
+    // (nor so small that o, at most 280 / factor, leaves fp32)
     const float s_win = a.window > 0 ? a.s_swa : a.s_sink, s_snk = n_sink > 0 ? a.s_sink : s_win;
-    const float lw = fmaxf(fabsf(a.scale) * s_win * kLog2e, 1e-30f), ls = fabsf(a.scale) * s_snk * kLog2e;
+    const float lw = fmaxf(fabsf(a.scale) * s_win * kLog2e, 1e-36f), ls = fabsf(a.scale) * s_snk * kLog2e;
     const float rs_w = 1.f / s_win, rs_s = 1.f / s_snk;
     const float s2w = ls / lw, o2w = (log2f(s_snk) - log2f(s_win)) / lw;   // a sink's S as a window row's of the same y
     bool ok = true;

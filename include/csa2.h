@@ -466,9 +466,12 @@ CSA2_API csa2_status csa2_pages_compact(const csa2_page_pool *pool, int32_t *n_l
  *         when that set is empty (a padded query: t = -1; t above 2^31 - 4,097 is
  *         taken as -1, CSA2_DEV_BAD_POSITION)
  *  ws, ws_bytes: csa2_prefix_attn_workspace_size(B, T_q, H, D) bytes
- * |q| must be below 65,504 (the products run in fp16).  Weights are rounded to
- * fp16 for the second product, the largest of a row lying at 2^9 or above: n
- * keys lose at most n 2^-34 of a row's weight.
+ * The products run in fp16 with every row of q multiplied by a power of two: q
+ * may be of any size, and rounding moves an element by 2^-23 of its row's
+ * largest at most.
+ * The logits have to be finite in FP32.  Weights are rounded to fp16 for the
+ * second product, the largest of a row lying at 2^9 or above: n keys lose at
+ * most n 2^-34 of a row's weight.
  * Supported: 1 <= H <= 64, B * T_q <= 65,535, window <= 1024.
  */
 CSA2_API csa2_status csa2_prefix_attn_decode(const csa2_page_pool *pool, const int32_t *seq, int n_shared,
@@ -489,7 +492,9 @@ CSA2_API size_t csa2_prefix_attn_workspace_size(int B, int T_q, int H, int D);
  *  q, q_pos, out as for entry 10; a query at t sees the tokens
  *         max(0,t-window+1)..t and the sinks before them (no token twice)
  *  ws, ws_bytes: csa2_window_attn_workspace_size(...) bytes
- * |q| must be below 65,504.
+ * q and the weights as for entry 10 (or held more precisely: windows whose rows
+ * fit shared memory take q as it is and the weights in two bf16 terms, so that
+ * the bits of an output can depend on B, T_q, H and the window).
  * Supported: 1 <= H <= 64, B * T_q <= 2^22, window <= 1024, at most 1024 sinks.
  */
 CSA2_API csa2_status csa2_window_attn(const csa2_swa_cache *swa, const csa2_swa_cache *sinks, const uint16_t *q,

@@ -138,3 +138,41 @@ def test_window_attention_keeps_the_tail_under_one_dominant_key(D, W):
     for b in range(2):
         check(out[b, 0], *attend64_tail(q[b, 0].double(), rows[b].double(), 1.0), f"b {b}")
     assert C.csa2_device_status() == 0
+
+
+# --------------------------------------------------------------------------- queries of any size
+# Each row of q is multiplied by a power of two that keeps its largest element at
+# 2^-2 or above, so rounding it to fp16 (2^-25 at most below the normal range; bf16
+# is exact above) moves an element by 2^-23 of the largest: a logit by 2^-23
+# max|q| sum|k| scale, a D-th or so of attend64's D 2^-23 sum|q k| scale.
+
+
+@pytest.mark.parametrize("size", [2.0 ** -30, 2.0 ** -100, 2.0 ** 40, 2.0 ** 90])
+@pytest.mark.parametrize("D,H", [(128, 8), (256, 20), (512, 64)])
+def test_queries_far_from_one(D, H, size):
+    """The normalisation may be folded into the softmax scale, with either sign."""
+    scale = 1.0 / math.sqrt(D) / size
+    run_prefix(D, H, 2, 16, 70, [90, 200], 40, seed=4, scale=scale, spread=size)
+    run_prefix(D, H, 1, 16, 70, [90, 200], 0, seed=5, scale=-scale, spread=size)
+    run_window(1, 9, H, D, 400, 4, 300, seed=6, scale=-scale, spread=size)        # rows that do not fit a ring
+    run_window(2, 70, H, D, 100, 4, 300, seed=7, scale=scale, spread=size)        # a resident ring
+
+
+@pytest.mark.parametrize("D", [128, 256, 512])
+def test_heads_of_very_different_sizes(D):
+    H, B, n = 64, 3, 500
+    pool, seq, values = paged_batch(D, D, 32, 400, [n, n - 50, 430])
+    g = gen(D + 1)
+    size = torch.exp2(torch.linspace(-60, -17, H, device="cuda")).view(1, 1, H, 1)
+    q = (torch.randn(B, 1, H, D, generator=g, device="cuda") * size).to(torch.bfloat16)
+    q[0, 0, 5], q[1, 0, 6] = 0, 0
+    q[0, 0, 7, 1:] = 0
+    rows = e4m3_rows(g, B, 1024, D)
+    out, scale = torch.empty_like(q), 2.0 ** 20 / math.sqrt(D)
+    C.csa2_prefix_attn_decode(pool, seq, 400, None, q, i32([[n]] * B), scale, out)
+    for b in range(B):
+        check(out[b, 0], *attend64(q[b, 0].double(), values[b], scale), f"prefix, b {b}")
+    C.csa2_window_attn(C.SwaCache.of(rows, scale=0.5, window=700), None, q, i32([[2000]] * B), scale, out)
+    for b in range(B):
+        check(out[b, 0], *attend64(q[b, 0].double(), window_keys(rows[b], 0.5, 2000, 700), scale), f"window, b {b}")
+    assert C.csa2_device_status() == 0
