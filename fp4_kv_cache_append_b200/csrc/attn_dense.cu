@@ -648,13 +648,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
       // A step's bytes.  The stage's step before may be the other team's: that
       // it has been consumed comes first, since the copies land in any order
       // and a wait for this step's phase, met in the phase before the last,
-      // would pass at once.  (The one before that has been consumed: this team
-      // has seen a step at most three back, which was loaded after it.)
+      // would pass at once.  The one before that, 2 x kStages back, has been
+      // consumed, or the first wait would pass a phase early too: a warp that
+      // asks for step n has seen its team's last one, s, and s was issued once
+      // step s - kStages had been consumed, so n - s <= kStages is needed.  The
+      // other team's steps in between are one group's: FP8_S at most.
       auto raw_wait = [&](uint32_t step) -> bool {
         const uint32_t st = step % kStages, ph = (step / kStages) & 1u;
         return all_wait(&S.raw_empty[st], ph ^ 1u) && all_wait(&S.raw_full[st], ph);
       };
       constexpr int FP8_S = GC / 2;                        // steps of a group of FP8 rows
+      static_assert(FP8_S + 1 <= kStages, "a team's next step is at most kStages behind its last");
 #pragma unroll 1
       for (int it = 0; it < n_tiles && ok; ++it) {
         const bool fp4 = it >= n_sink && it < n_sink + n_fp4;

@@ -176,3 +176,108 @@ def test_heads_of_very_different_sizes(D):
     for b in range(B):
         check(out[b, 0], *attend64(q[b, 0].double(), window_keys(rows[b], 0.5, 2000, 700), scale), f"window, b {b}")
     assert C.csa2_device_status() == 0
+
+
+# --------------------------------------------------------------------------- every launch, bit by bit
+# The stages that a block's two teams share are met in every order of arrival; a
+# step that is read too early or too late is off by less than other tests allow.
+
+
+def _launches(call, like, n=1000, at_once=50):
+    first = torch.empty_like(like)
+    call(first)
+    outs = torch.empty(at_once, *like.shape, dtype=like.dtype, device="cuda")
+    for _ in range(n // at_once):
+        for o in outs:
+            call(o)
+        assert not bool((outs != first).any())
+    assert C.csa2_device_status() == 0
+    return first
+
+
+@pytest.mark.parametrize("B,T,H,D,window,n_sink", [
+    (2, 5, 64, 512, 1024, 64),        # many tiles of FP8 rows, both channel halves
+    (16, 1, 64, 512, 128, 4),         # single tokens: no resident ring
+    (3, 60, 64, 512, 300, 70),        # 180 units: a second one to some blocks
+    (4, 60, 16, 256, 500, 0),
+    (2, 200, 16, 128, 900, 9),
+])
+def test_windows_of_many_tiles_give_the_same_bits_in_every_launch(B, T, H, D, window, n_sink):
+    g = gen(T + window)
+    swa = C.SwaCache.of(e4m3_rows(g, B, window + T - 1 + 40, D), scale=0.75, window=window)
+    sinks = C.SwaCache.of(e4m3_rows(g, B, n_sink, D), scale=1.25, window=n_sink) if n_sink else None
+    q = torch.randn(B, T, H, D, generator=g, device="cuda").to(torch.bfloat16)
+    pos = i32([[3000 + 13 * b + j for j in range(T)] for b in range(B)])
+    scale = 1.0 / math.sqrt(D)
+    out = _launches(lambda o: C.csa2_window_attn(swa, sinks, q, pos, scale, o), q)
+    for b, j in ((0, 0), (B - 1, T - 1), (B // 2, T // 2)):
+        t = int(pos[b, j])
+        keys = [window_keys(swa.rows[b], 0.75, t, window)]
+        if n_sink:
+            keys.append(sinks.rows[b].view(torch.float8_e4m3fn).double() * 1.25)
+        check(out[b, j], *attend64(q[b, j].double(), torch.cat(keys), scale), f"b {b} query {j}")
+
+
+@pytest.mark.parametrize("D,window", [(512, 1000), (256, 600), (128, 1000)])
+def test_entries_and_a_window_of_many_tiles_give_the_same_bits_in_every_launch(D, window):
+    """FP4 steps, then FP8 steps of the same stages, over and over."""
+    B, H, n_shared = 6, 48, 257
+    pool, seq, values = paged_batch(D, D, 64, n_shared, [n_shared + 70 * b + 1 for b in range(B)])
+    g = gen(D + window)
+    swa = C.SwaCache.of(e4m3_rows(g, B, window + 9, D), scale=0.5, window=window)
+    q = torch.randn(B, 2, H, D, generator=g, device="cuda").to(torch.bfloat16)
+    pos = i32([[2000 + b, 2001 + b] for b in range(B)])
+    ws = C.workspace(C.csa2_prefix_attn_workspace_size(B, 2, H, D))
+    out = _launches(lambda o: C.csa2_prefix_attn_decode(pool, seq, n_shared, swa, q, pos, 0.05, o, ws=ws), q)
+    for b in range(B):
+        keys = torch.cat([values[b], window_keys(swa.rows[b], 0.5, 2001 + b, window)])
+        check(out[b, 1], *attend64(q[b, 1].double(), keys, 0.05), f"b {b}")
+
+
+# --------------------------------------------------------------------------- blocks with several units
+
+
+@pytest.mark.parametrize("B,T,H,D,window,n_sink,start", [
+    (3, 140, 64, 512, 200, 4, 90),        # no ring: 420 units of a channel half on the SMs
+    (5, 90, 64, 256, 300, 20, 0),         # 225 units
+    (7, 101, 40, 128, 512, 3, 400),       # 224 units, odd rows
+    (40, 3, 64, 512, 1024, 5, 2000),      # 160 units, no sequence twice in a block
+])
+def test_windows_without_a_ring_over_several_units(B, T, H, D, window, n_sink, start):
+    run_window(B, T, H, D, window, n_sink, start, seed=B, poison=True)
+
+
+@pytest.mark.parametrize("B,T,H,D,window,n_sink,start", [
+    (1, 500, 64, 512, 128, 4, 1000),      # 250 tiles: a block walks along a sequence
+    (5, 130, 64, 512, 100, 4, 50),        # 325 tiles: blocks cross from one sequence to the next
+    (60, 9, 64, 512, 128, 0, 700),        # 300 tiles of 60 sequences
+    (11, 77, 20, 256, 128, 9, 0),         # tiles across queries, ragged ends
+    (33, 40, 16, 128, 130, 4, 60),
+    (9, 300, 8, 128, 60, 5, 5),
+])
+def test_resident_rings_over_several_units_and_sequences(B, T, H, D, window, n_sink, start):
+    run_window(B, T, H, D, window, n_sink, start, seed=T, poison=True)
+
+
+@pytest.mark.parametrize("B,H,D,window,n_sink", [(148, 64, 512, 128, 4), (75, 64, 512, 128, 4), (512, 64, 512, 128, 4),
+                                                 (300, 17, 512, 50, 0), (700, 16, 256, 16, 4), (400, 64, 128, 30, 2)])
+def test_single_tokens_of_many_sequences(B, H, D, window, n_sink):
+    """Large decode batches of a window-only layer, each sequence at its own place, some padded."""
+    rng = np.random.default_rng(B)
+    pos = [[-1 if b % 17 == 5 else int(rng.integers(0, 3 * window if b % 2 else 100000))] for b in range(B)]
+    run_window(B, 1, H, D, window, n_sink, 0, seed=B, q_pos=pos, poison=True)
+
+
+# --------------------------------------------------------------------------- chunks over pages
+
+
+@pytest.mark.parametrize("D,H,T,page,n_shared,lens,window,m", [
+    (512, 64, 40, 64, 130, [400, 333], 128, 1),
+    (512, 16, 70, 32, 0, [71, 300], 0, 2),
+    (256, 20, 65, 48, 100, [300, 165, 129], 90, 1),
+    (128, 8, 100, 16, 64, [700, 164], 128, 2),
+    (128, 64, 33, 128, 0, [33, 34, 500], 0, 1),
+])
+def test_prefix_attention_of_prompt_chunks(D, H, T, page, n_shared, lens, window, m):
+    """Many queries of a sequence at once, each seeing the entries up to its own."""
+    run_prefix(D, H, T, page, n_shared, lens, window, m=m, seed=T, poison=True)
