@@ -128,7 +128,7 @@ struct Cfg {
 // What a block does next: a part of a unit's key list.
 struct Segment {
   int half;                // channel half
-  int b;                   // batch row of the keys (0 over the shared prefix)
+  int b;                   // batch row of the window rows (0 over the shared prefix)
   int row0;                // first flattened row
   int nrows;
   int n_sink, n_fp4, n_win;   // tiles of each sort, in this order
@@ -308,10 +308,13 @@ __device__ __forceinline__ int seq_entries(const DenseAttnArgs &a, int b, int *n
   *n = v < 0 ? 0 : (v > room ? (int)room : v);
   return s;
 }
+__device__ __forceinline__ int tiles_of(const DenseAttnArgs &a, const Schedule &s, int n) {
+  return n > a.n_shared ? (n - s.own0 + kTile - 1) / kTile : 0;
+}
 __device__ __forceinline__ int own_tiles(const DenseAttnArgs &a, const Schedule &s, int b) {
   int n;
   seq_entries(a, b, &n);
-  return n > a.n_shared ? (n - s.own0 + kTile - 1) / kTile : 0;
+  return tiles_of(a, s, n);
 }
 
 // Workspace: per unit {first slot, slots}; per slot of a unit of the prefix (0)
@@ -344,9 +347,10 @@ struct Cursor {
   long long at;
 };
 
-// Warp 0: the segment at linear position *x (before x_end); advances *x.
+// The scheduler's warp: the segment at linear position *x (before x_end); advances
+// *x.  `lead`: the batch row through whose table the prefix is read.
 template <int DO>
-__device__ __forceinline__ bool next_prefix_segment(const DenseAttnArgs &a, const Schedule &sc, long long th, long long chunk,
+__device__ __forceinline__ bool next_prefix_segment(const DenseAttnArgs &a, const Schedule &sc, int lead, long long th, long long chunk,
                                     long long *x, long long x_end, int lane, Cursor &cur, Segment &sg) {
 #pragma unroll 1
   while (*x < x_end) {
@@ -423,13 +427,13 @@ __device__ __forceinline__ bool next_prefix_segment(const DenseAttnArgs &a, cons
         sg.nrows = rows - rt * kRows < kRows ? rows - rt * kRows : kRows;
       }
       int ents = 0;
-      sg.seq = seq_entries(a, shared ? 0 : b, &ents);
+      sg.seq = seq_entries(a, shared ? lead : b, &ents);
       sg.n_sink = 0;
       sg.n_fp4 = (int)n;
       sg.n_win = win ? 1 : 0;   // counted below
       sg.key0 = (shared ? 0 : sc.own0) + (int)tile * kTile;
       sg.key_lo = shared ? 0 : a.n_shared;
-      sg.key_end = shared ? a.n_shared : ents;
+      sg.key_end = shared && ents > a.n_shared ? a.n_shared : ents;
       const int u = half * sc.units + unit;
       const int g0 = (int)div64(unit_at + sc.ov, chunk);
       // (a unit's parts lie in consecutive blocks, and the next unit starts in
@@ -1049,9 +1053,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
       // work is [x, x_end) of the tiles' linear order (prefix), every grid-th unit (window)
       long long th = 0, chunk = 1, x, x_end;
       Cursor cur{-1, 0, 0};
+      int lead = 0;
       if (MODE == 0) {
+        // the prefix is read through the first sequence that holds most of it, of
+        // those with a query (a padded row may name any sequence)
         long long sum = 0;
-        for (int b = lane; b < a.B; b += 32) sum += own_length(sc, own_tiles(a, sc, b));
+        int most = -1, first = 0;
+        for (int b = lane; b < a.B; b += 32) {
+          int n;
+          seq_entries(a, b, &n);
+          sum += own_length(sc, tiles_of(a, sc, n));
+          n = n < a.n_shared ? n : a.n_shared;
+          if (n > most) {
+            int j = 0;
+#pragma unroll 1
+            while (j < a.T_q && a.q_pos[(size_t)b * a.T_q + j] < 0) ++j;
+            if (j < a.T_q) {
+              most = n;
+              first = b;
+            }
+          }
+        }
+        const int top = __reduce_max_sync(0xffffffffu, most);
+        lead = __reduce_min_sync(0xffffffffu, most == top ? first : INT_MAX);
 #pragma unroll 1
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         th = sc.rt_sh * shared_length(sc) + sc.rt_own * sum;
@@ -1066,7 +1090,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
         Segment &sg = S.seg[i & 1u];
         bool more;
         if (MODE == 0) {
-          more = next_prefix_segment<DO>(a, sc, th, chunk, &x, x_end, lane, cur, sg);
+          more = next_prefix_segment<DO>(a, sc, lead, th, chunk, &x, x_end, lane, cur, sg);
         } else {
           more = x < x_end;
           if (more && lane == 0) {

@@ -453,10 +453,11 @@ CSA2_API csa2_status csa2_pages_compact(const csa2_page_pool *pool, int32_t *n_l
  *     once for the whole batch.
  *  pool   the entries; seq [B] i32 DEVICE: pool sequence of each batch row
  *  n_shared (host) entries that the batch's sequences have in common: they are
- *         read once, through the table of seq[0], which holds them all (0 =
- *         nothing is shared).  That the sequences agree on them is the
- *         caller's word; a sequence with fewer entries sees only its own
- *         number of them.
+ *         read once, through the table of the first sequence that holds most of
+ *         them (0 = nothing is shared).  That the sequences agree on them is the
+ *         caller's word; a sequence with fewer entries sees only its own number
+ *         of them.  Rows without a query (every t negative) are not asked and
+ *         may name any sequence, or -1.
  *  swa    window cache of the layer with B rows (NULL: no window); its
  *         W_cap >= T_q + window - 1, as for the append
  *  q      [B][T_q][H][D] bf16, q_pos [B][T_q] i32 token position t of each query

@@ -281,3 +281,58 @@ def test_single_tokens_of_many_sequences(B, H, D, window, n_sink):
 def test_prefix_attention_of_prompt_chunks(D, H, T, page, n_shared, lens, window, m):
     """Many queries of a sequence at once, each seeing the entries up to its own."""
     run_prefix(D, H, T, page, n_shared, lens, window, m=m, seed=T, poison=True)
+
+
+# --------------------------------------------------------------------------- padded batches
+
+
+@pytest.mark.parametrize("D,H,T,n_shared,window,first", [(128, 8, 1, 300, 128, "none"), (512, 64, 1, 300, 0, "none"),
+                                                         (256, 20, 3, 129, 40, "other"), (512, 16, 2, 64, 9, "short"),
+                                                         (128, 64, 2, 65, 0, "empty")])
+def test_prefix_is_read_whatever_the_first_row_is(D, H, T, n_shared, window, first):
+    """A batch whose first slot is padded (no sequence, or some other one), empty,
+    or shorter than the prefix."""
+    lens = [n_shared + 50, n_shared + 1, n_shared - 20, n_shared + 130]
+    pool, seq, values = paged_batch(D + T, D, 32, n_shared, lens)
+    g = gen(D)
+    spare = next(s for s in range(pool.n_seq) if s not in seq.tolist())
+    if first == "other":                                      # as long, of other entries
+        pool.table[spare, :] = torch.arange(pool.max_pages, device="cuda").flip(0) % pool.n_pages
+        pool.n_entries[spare] = n_shared + 5
+    order = [2, 0, 1, 3] if first == "short" else [0, 1, 2, 3]
+    rows_seq = [int(seq[i]) for i in order]
+    keys = [values[i] for i in order]
+    n_of = [lens[i] for i in order]
+    if first != "short":
+        rows_seq = [{"none": -1, "other": spare, "empty": spare}[first]] + rows_seq
+        keys, n_of = [keys[0][:0]] + keys, [0] + n_of
+    B = len(rows_seq)
+    pos = [[n - T + j for j in range(T)] for n in n_of]
+    if first in ("none", "other"):
+        pos[0] = [-1] * T
+    q = torch.randn(B, T, H, D, generator=g, device="cuda").to(torch.bfloat16)
+    rows = e4m3_rows(g, B, window + T + 2, D) if window else None
+    swa = C.SwaCache.of(rows, scale=0.5, window=window) if window else None
+    buf, out = guarded((B, T, H, D))
+    C.csa2_prefix_attn_decode(pool, i32(rows_seq), n_shared, swa, q, i32(pos), 0.06, out)
+    for b in range(B):
+        for j in range(T):
+            t = pos[b][j]
+            k = [keys[b][: max(0, t + 1)]]
+            if window and t >= 0:
+                k.append(window_keys(rows[b], 0.5, t, window))
+            check(out[b, j], *attend64(q[b, j].double(), torch.cat(k), 0.06), f"b {b} query {j}")
+    assert bool((buf[:1024] == 7).all()) and bool((buf[-1024:] == 7).all())
+    assert C.csa2_device_status() == 0
+
+
+def test_prefix_longer_than_every_sequence():
+    D, H = 256, 8
+    pool, seq, values = paged_batch(3, D, 16, 100, [100, 40])
+    q = torch.randn(2, 1, H, D, generator=gen(3), device="cuda").to(torch.bfloat16)
+    out = torch.empty_like(q)
+    for order in ([0, 1], [1, 0]):
+        C.csa2_prefix_attn_decode(pool, seq[order].contiguous(), 112, None, q, i32([[500], [500]]), 0.06, out)
+        for b, i in enumerate(order):
+            check(out[b, 0], *attend64(q[b, 0].double(), values[i], 0.06), f"b {b}")
+    assert C.csa2_device_status() == 0
