@@ -181,7 +181,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const AttnArgs a) {
   const int split = blockIdx.y;
   const int b = row / a.T_q;
   const int mt_lo = (int)blockIdx.z * (MT / a.csplit), mt_hi = mt_lo + MT / a.csplit;   // O^T blocks of this block
-  pdl_launch_dependents();
 
   // ---- set-up that touches no global memory overlaps the previous kernel
   if (tid == 0) {
@@ -201,6 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_kernel(const AttnArgs a) {
   if (warp == kMmaWarp) {
     tmem_alloc(&S.tmem_base, kTmemCols);
     tmem_relinquish();
+    pdl_launch_dependents();   // (only now: see pdl_launch_dependents)
   }
   tc_fence_before();
   __syncthreads();

@@ -506,7 +506,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
                                                      ~uintptr_t(1023));
   volatile int *abort = &S.abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  pdl_launch_dependents();
   if (tid == 0) {
     for (int g = 0; g < NG; ++g) {
       mbar_init(&S.full[g], kTeam);
@@ -530,6 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
   if (warp == kMmaWarp) {
     tmem_alloc(&S.tmem_base, kTmemCols);
     tmem_relinquish();
+    pdl_launch_dependents();   // (only now: see pdl_launch_dependents)
   }
   tc_fence_before();
   __syncthreads();

@@ -191,7 +191,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_lat_kernel(const AttnArgs a)
   const int split = blockIdx.y;
   const int b = row / a.T_q;
   const int mt_lo = (int)blockIdx.z * (MT / a.csplit), mt_hi = mt_lo + MT / a.csplit;   // O^T blocks of this block
-  pdl_launch_dependents();
 
   // ---- set-up that touches no global memory overlaps the previous kernel
   if (tid == 0) {
@@ -203,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_lat_kernel(const AttnArgs a)
   if (warp == kMmaWarp) {
     tmem_alloc(&S.tmem_base, kCols);
     tmem_relinquish();
+    pdl_launch_dependents();   // (only now: see pdl_launch_dependents)
   }
   // ---- Q: bf16 -> fp16 into the B-operand layout.  The query and its
   // position are inputs of the call that no launch of this library writes, so

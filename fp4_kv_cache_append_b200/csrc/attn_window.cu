@@ -119,7 +119,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
   volatile int *abort = &S.abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n_sink = a.n_sink, rw = R - n_sink > 0 ? R - n_sink : 1;   // ring: slots [0, n_sink) sinks, then token mod rw
-  pdl_launch_dependents();
   if (tid == 0) {
     for (int i = 0; i < QSL; ++i) { mbar_init(&S.q_full[i], 1); mbar_init(&S.q_empty[i], 1); }
     for (int i = 0; i < 4; ++i) mbar_init(&S.k_full[i], 1);
@@ -140,6 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
   if (warp == kMmaWarp) {
     tmem_alloc(&S.tmem_base, kTmemCols);
     tmem_relinquish();
+    pdl_launch_dependents();   // (only now: see pdl_launch_dependents)
   }
   tc_fence_before();
   __syncthreads();
