@@ -247,18 +247,22 @@ class PagePool:
         return c
 
     def _set(self, codes, scales, refs, table, n_entries, m):
-        n_pages, page, half = codes.shape
-        D = 2 * half
-        n_seq, max_pages = table.shape
-        for t, dtype, shape in ((codes, torch.uint8, (n_pages, page, half)),
-                                (scales, torch.uint8, (n_pages, page, D // 16)),
-                                (refs, torch.int32, (n_pages,)), (table, torch.int32, (n_seq, max_pages)),
-                                (n_entries, torch.int32, (n_seq,))):
-            if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != codes.device:
-                raise ValueError(f"page pool planes: expected contiguous {dtype} {shape} on {codes.device}, got "
-                                 f"{t.dtype} {tuple(t.shape)} on {t.device}")
         self.codes, self.scales, self.refs, self.table, self.n_entries = codes, scales, refs, table, n_entries
-        self.n_pages, self.page, self.n_seq, self.max_pages, self.D, self.m = n_pages, page, n_seq, max_pages, D, m
+        self.n_pages, self.page, half = codes.shape
+        self.n_seq, self.max_pages = table.shape
+        self.D, self.m = 2 * half, m
+        self._check()
+
+    def _check(self):
+        n_pages, page, n_seq = self.n_pages, self.page, self.n_seq
+        for t, dtype, shape in ((self.codes, torch.uint8, (n_pages, page, self.D // 2)),
+                                (self.scales, torch.uint8, (n_pages, page, self.D // 16)),
+                                (self.refs, torch.int32, (n_pages,)),
+                                (self.table, torch.int32, (n_seq, self.max_pages)),
+                                (self.n_entries, torch.int32, (n_seq,))):
+            if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != self.codes.device:
+                raise ValueError(f"page pool planes: expected contiguous {dtype} {shape} on {self.codes.device}, got "
+                                 f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
     def __setattr__(self, name, value):   # any change rebuilds the descriptor
         object.__setattr__(self, name, value)
@@ -268,6 +272,7 @@ class PagePool:
         if _elsewhere(self.codes.device):
             _check_device(self.codes.device, "the pool's planes")
         if self._desc is None:
+            self._check()   # planes can be replaced; the kernels' bounds come from the sizes
             object.__setattr__(self, "_desc", PagePoolDesc(
                 self.codes.data_ptr(), self.scales.data_ptr(), self.refs.data_ptr(), self.table.data_ptr(),
                 self.n_entries.data_ptr(), self.n_pages, self.page, self.n_seq, self.max_pages, self.D, self.m))
