@@ -836,6 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
         unpow = __uint_as_float((254u - qf) << 23);
         tmem_wait_st();
       }
+      const float lscale = fabsf(a.scale) * kLog2e * unpow;   // of a logit in base 2, but for the key's scale
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -894,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
         if (!ok) break;
         tc_fence_after();
         // logits in base 2: lsc x S; never 0, so that a hidden key's -inf stays
-        const float lsc = fmaxf(fabsf(a.scale) * ksc * kLog2e * unpow, 1e-30f);
+        const float lsc = fmaxf(lscale * ksc, 1e-30f);
         uint32_t sv[kTile];
         tmem_ld_x32(scol, sv);
         tmem_ld_x32(scol + 32, sv + 32);

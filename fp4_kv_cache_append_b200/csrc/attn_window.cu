@@ -68,7 +68,7 @@ struct Pass {
   int more;                // 0: no further pass
   int row0, nrows, b;
   int q0, nq;
-  int lo, end;             // tokens [lo, end) that the covered queries see (none: end <= lo)
+  int end;                 // the covered queries see tokens below this one
   int from;                // queries before this token were covered by an earlier pass of the tile
   int first;               // first pass of the tile (it also covers padded queries)
   int load_lo;             // window rows [load_lo, end) enter the ring
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
       const int frow = ps.row0 + row;
       const bool live = row < ps.nrows;
       const int t = live ? ps.pos[frow / a.H - ps.q0] : -1;
-      // covered by this pass: its window lies in [lo, end) and no earlier pass covered it
+      // covered by this pass: its window ends in [from, end), so no earlier pass covered it
       const bool mine = live && (t < 0 ? ps.first != 0 : (t >= ps.from && t < ps.end));
       // the slots this row sees, one bit per key
       int wlo = a.window > 0 ? t - a.window + 1 : t + 1;
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_window_kernel(const DenseAtt
             }
             if (lane == 0) {
               ps.more = 1; ps.row0 = row0; ps.nrows = nrows; ps.b = b; ps.q0 = q0; ps.nq = nq;
-              ps.lo = lo; ps.end = end; ps.from = from; ps.first = first;
+              ps.end = end; ps.from = from; ps.first = first;
               ps.load_lo = load_lo; ps.load_sinks = !none && b != res_b; ps.wait_for = wait_for;
               ps.cold = same ? 0 : cold;
             }
