@@ -54,8 +54,8 @@
 // exits.
 //
 // What bounds it (D 512, H 64, 32 sequences of one token, 65,536 shared entries
-// and 512 to 1,024 own ones: 334 us alone, 367 us in a long loop, where the power
-// limit holds the SMs near 1.6 GHz; 755 TFLOP/s of the 4 D FLOP per row and
+// and 512 to 1,024 own ones: 320 to 335 us alone, 363 to 375 us in a long loop,
+// where the power limit holds the SMs near 1.6 GHz; 755 TFLOP/s of the 4 D FLOP per row and
 // key): shared memory.  A tile of 64 keys and a channel half moves 260 KB through
 // it (S with Q in shared memory 96, in tensor memory 32, O 32, the fp16 keys
 // written 64, the raw bytes in and out 36; the bank counters say the same): 2,030
@@ -63,7 +63,7 @@
 // the tensor core is busy for 1,830 of them.  For D 128 and 256 all of Q is in
 // tensor memory and the softmax's own chain (about 1,650 cycles a tile: 64
 // exponentials on a scheduler's pipe take 512) is the longest: the same case at D
-// 256 takes 127 us (1,100 TFLOP/s), with 32 heads of D 128 70 us.
+// 256 takes 129 us (1,080 TFLOP/s), with 32 heads of D 128 71 us.
 // Loads with a copy instruction per 16 bytes (cp.async) took 2,560 cycles of the
 // loading warp per tile, more than the tile itself: 424 us against 384 us then.
 // A softmax split over two threads per row halves its arithmetic but has them
@@ -89,8 +89,10 @@ constexpr int kThreads = 16 * 32;            // four warpgroups: registers are s
 constexpr int kSegBar = 1, kQBar = 2, kQTopBar = 3;
 constexpr int kSchedWarp = 15;               // writes the next segment
 // Registers per thread of the warpgroups: 2 x fetch, softmax, MMA (a tile's
-// logits stay in registers; a spill would go to L2, shared memory takes all of
-// the L1's room).  Their sum is at most the launch's 4 x 128.
+// logits stay in registers; what is spilled goes to L2, since shared memory takes
+// all of the L1's room: at D 128 and in the paged D 512 kernel one word a thread,
+// written once and read in four or five places).  Their sum is at most the
+// launch's 4 x 128.
 constexpr int kRegsFetch = 88, kRegsSoftmax = 208, kRegsMma = 128;
 constexpr int kLoadWarp = 13;                // loader
 constexpr int kPvWarp = 14;                  // MMA issuer of O (kMmaWarp: of S)
@@ -98,8 +100,9 @@ constexpr int kStages = 3;                   // raw steps in flight or in use
 // A stage: 64 rows of 128 bytes (codes, 64 bytes for D 128, or FP8 values),
 // then 64 rows of scales (16 bytes, 8 for D 128).
 constexpr int kRawRow = 128, kRawSc = kTile * kRawRow, kRawBytes = kRawSc + kTile * 16;
-// A unit's start and end in tiles (see Schedule::ov): the case above takes 427 us
-// with 2, 363 with 5, 343 with 8, 345 with 10 and 349 with 16.
+// A unit's start and end in tiles (see Schedule::ov), fitted at D 512: the case
+// above takes 427 us with 2, 363 with 5, 343 with 8, 345 with 10 and 349 with 16.
+// (At D 128 and 256, where a tile takes less, it was not fitted.)
 constexpr int kUnitCost = 8;
 // P = 2^(x - reference + kBias), at most 2^(kBias + kLazy) = 61,147, below fp16's
 // 65,504.  The row's largest weight is then at least 2^9, weights down to 2^-23

@@ -18,9 +18,9 @@
 // tensor-memory columns and stored as it is formed.  What is left is the traffic
 // of q and the output, 4 bytes per (row, channel): 132 FLOP per byte at a window
 // of 128 and D 512.
-// 8,192 tokens of 64 heads, D 512, window 128 and 4 sinks: 234 us alone = 4.6 TB/s
-// (164 us of traffic at the copy rate), tensor core 47% busy; 275 us in a long
-// loop, where the power limit holds the SMs near 1.35 GHz.  With P in one term the
+// 8,192 tokens of 64 heads, D 512, window 128 and 4 sinks: 223 to 244 us alone =
+// 4.4 to 4.8 TB/s (164 us of traffic at the copy rate), tensor core 48% busy; 270
+// to 288 us in a long loop, where the power limit holds the SMs near 1.35 GHz.  With P in one term the
 // loop takes 248 us, at 2^-9 instead of 2^-17 of P.
 // Warp roles, all persistent, handing work over through mbarriers:
 //   warps 0-3, 4-7    softmax, one row per thread, each group half of the keys
@@ -689,10 +689,11 @@ static cudaError_t launch_t(const CUtensorMap &q_map, const DenseAttnArgs &a, in
 // has two blocks for a tile of D 512 and starts sooner, is ahead, unless its
 // second block makes a second wave or all keys are one tile of its own.  us,
 // resident | other, one token of H heads, window 128 and 4 sinks: B 16 H 64 D 512
-// 16.2 | 14.6, B 74 17.0 | 15.9, B 148 19.1 | 28.5; H 16 D 256 B 64 14.1 | 12.8,
-// B 600 54.7 | 45.7 (window of 16: 34.4 | 40.3); H 64 D 128 B 148 13.2 | 10.8,
-// B 1,000 65.8 | 53.9.  Chunks of tokens: 8 x 8, H 64 D 512 16.6 | 17.3; 64 x 4
-// 18.7 | 32.4; 1 x 8,192 234 | 786; H 8 D 128 34.3 | 36.4.
+// 16.1 | 14.9, B 74 16.6 | 16.5, B 148 19.0 | 29.7, B 512 66.9 | 99.4; H 16 D 256
+// B 64 13.9 | 12.0, B 600 54.9 | 47.0 (window of 16: 35.6 | 42.4); H 64 D 128
+// B 148 13.2 | 11.0, B 1,000 66.4 | 55.4.  Chunks of tokens: 8 x 8, H 64 D 512
+// 16.6 | 17.7; 64 x 4 18.8 | 33.1; 1 x 8,192 228 | 796.  (Where it does not hold:
+// few heads of D 128, 1 x 8,192, H 8 39.9 | 36.4 and 1 x 1,024 14.2 | 10.7.)
 bool window_takes_ring(const DenseAttnArgs &a, int sms) {
   const int keys = a.n_sink + (a.window > 0 ? a.window + tile_queries(a) - 1 : 0);
   if (keys > ring_keys(a.D)) return false;

@@ -9,10 +9,12 @@
 // sequence) plan and a wide copy, chained by programmatic dependent launch, but
 // for short fork lists (one launch).
 // Measured: compacting 8,192 pages of 128 entries, D 512, half of them live (2,048
-// move, 151 MB): plan 6 us, move 26 us = 5.8 TB/s, 88% of a plain copy.  Appending
-// 49,152 entries (28 MB): plan 7.7 us, copies 8.4 us alone, 11 us a call back to
-// back.  One entry for each of 32 sequences: 10 us, which the host takes for the
-// call and its two launches.
+// move, 151 MB): plan 6 us, move 26 us = 5.8 TB/s, 88% of a plain copy.  Appends,
+// a call in a replayed graph, first into pages that the sequences hold alone, then
+// with the pool as it was before (fresh pages, shared last pages copied): 49,152
+// entries (28 MB) 9.5 and 8.8 us, one entry for each of 32 sequences 6.7 and 8.4
+// us.  Back to back from the host 10 to 11 us, which it takes for a call and its
+// two launches.
 #include "common.cuh"
 #include "kernels_paged.h"
 
@@ -346,7 +348,7 @@ __device__ __forceinline__ bool pair_sets(const PageForkArgs &a, int j, int c) {
 // Short lists: one cluster, pair i in block i % 8, with a cluster barrier between
 // the two halves and the taken rows in registers.  One launch instead of two:
 // 6.9 us a call instead of 9.8 (8 sequences of 40 pages, back to back: what the
-// host takes for it).
+// host takes for it; 3.9 us in a replayed graph).
 constexpr int kForkBlocks = 8, kForkSlots = 8;   // blocks of the cluster; slots per thread
 __global__ void __launch_bounds__(kPlanThreads) page_fork_kernel(const PageForkArgs a) {
   const PagePoolArgs &P = a.pool;

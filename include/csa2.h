@@ -492,7 +492,8 @@ CSA2_API size_t csa2_prefix_attn_workspace_size(int B, int T_q, int H, int D);
  *         the sequence's first tokens arrive); its own scale
  *  q, q_pos, out as for entry 10; a query at t sees the tokens
  *         max(0,t-window+1)..t and the sinks before them (no token twice)
- *  ws, ws_bytes: csa2_window_attn_workspace_size(...) bytes
+ *  ws, ws_bytes: csa2_window_attn_workspace_size(...) bytes (0 for every shape so
+ *         far: ws may then be NULL)
  * q and the weights as for entry 10 (or held more precisely: windows whose rows
  * fit shared memory take q as it is and the weights in two bf16 terms, so that
  * the bits of an output can depend on B, T_q, H and the window).
