@@ -532,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
   if (warp == kMmaWarp) {
     tmem_alloc(&S.tmem_base, kTmemCols);
     tmem_relinquish();
-    pdl_launch_dependents();   // (only now: see pdl_launch_dependents)
+    pdl_launch_dependents();   // behind the allocation: a dependent on this SM that allocated first would wait for this grid
   }
   tc_fence_before();
   __syncthreads();

@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_lat_kernel(const AttnArgs a)
   if (warp == kMmaWarp) {
     tmem_alloc(&S.tmem_base, kCols);
     tmem_relinquish();
-    pdl_launch_dependents();   // (only now: see pdl_launch_dependents)
+    pdl_launch_dependents();   // behind the allocation: a dependent on this SM that allocated first would wait for this grid
   }
   // ---- Q: bf16 -> fp16 into the B-operand layout.  The query and its
   // position are inputs of the call that no launch of this library writes, so

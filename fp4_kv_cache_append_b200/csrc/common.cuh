@@ -91,9 +91,6 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
 // previous kernel of the stream drains: pdl_wait() returns once that grid has
 // completed and its memory is visible (a no-op without the attribute), and
 // pdl_launch_dependents() lets the next kernel of the stream launch early.
-// A kernel that uses tensor memory calls it from the allocating warp, behind the
-// allocation: a dependent that shares the SM and allocates first would hold the
-// columns until this grid completes, while this grid waits for them.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
