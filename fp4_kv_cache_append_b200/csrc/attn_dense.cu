@@ -55,8 +55,8 @@
 //
 // What bounds it (D 512, H 64, 32 sequences of one token, 65,536 shared entries
 // and 512 to 1,024 own ones: 320 to 335 us alone, 363 to 375 us in a long loop,
-// where the power limit holds the SMs near 1.6 GHz; 755 TFLOP/s of the 4 D FLOP per row and
-// key): shared memory.  A tile of 64 keys and a channel half moves 260 KB through
+// where the power limit holds the SMs near 1.6 GHz; 755 TFLOP/s of the 4 D FLOP
+// per row and key): shared memory.  A tile of 64 keys and a channel half moves 260 KB through
 // it (S with Q in shared memory 96, in tensor memory 32, O 32, the fp16 keys
 // written 64, the raw bytes in and out 36; the bank counters say the same): 2,030
 // cycles at the 128 bytes a cycle that the S product reaches, of 2,350 measured;
@@ -353,8 +353,8 @@ struct Cursor {
 // The scheduler's warp: the segment at linear position *x (before x_end); advances
 // *x.  `lead`: the batch row through whose table the prefix is read.
 template <int DO>
-__device__ __forceinline__ bool next_prefix_segment(const DenseAttnArgs &a, const Schedule &sc, int lead, long long th, long long chunk,
-                                    long long *x, long long x_end, int lane, Cursor &cur, Segment &sg) {
+__device__ __forceinline__ bool next_prefix_segment(const DenseAttnArgs &a, const Schedule &sc, int lead, long long th,
+                                    long long chunk, long long *x, long long x_end, int lane, Cursor &cur, Segment &sg) {
 #pragma unroll 1
   while (*x < x_end) {
     const int half = *x >= th ? 1 : 0;   // at most two channel halves

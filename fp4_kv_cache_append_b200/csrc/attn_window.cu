@@ -20,8 +20,8 @@
 // of 128 and D 512.
 // 8,192 tokens of 64 heads, D 512, window 128 and 4 sinks: 223 to 244 us alone =
 // 4.4 to 4.8 TB/s (164 us of traffic at the copy rate), tensor core 48% busy; 270
-// to 288 us in a long loop, where the power limit holds the SMs near 1.35 GHz.  With P in one term the
-// loop takes 248 us, at 2^-9 instead of 2^-17 of P.
+// to 288 us in a long loop, where the power limit holds the SMs near 1.35 GHz.
+// With P in one term the loop takes 248 us, at 2^-9 instead of 2^-17 of P.
 // Warp roles, all persistent, handing work over through mbarriers:
 //   warps 0-3, 4-7    softmax, one row per thread, each group half of the keys
 //                (they exchange the row maxima); P replaces S in tensor memory

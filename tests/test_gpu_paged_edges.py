@@ -336,3 +336,85 @@ def test_prefix_longer_than_every_sequence():
         for b, i in enumerate(order):
             check(out[b, 0], *attend64(q[b, 0].double(), values[i], 0.06), f"b {b}")
     assert C.csa2_device_status() == 0
+
+
+@pytest.mark.parametrize("D,H,B,window", [(128, 64, 150, 40), (256, 33, 90, 0), (512, 64, 80, 128)])
+def test_powers_of_two_of_the_queries_change_no_bit(D, H, B, window):
+    """q x 2^20 and q x 2^-30 are both brought to [2^14, 2^15), and the softmax
+    scale takes the powers back exactly; units and segments by the hundred."""
+    lens = [200 + 3 * i for i in range(20)]
+    pool, seq, _ = paged_batch(D, D, 32, 150, lens)
+    many = seq[torch.arange(B, device="cuda") % 20].contiguous()
+    g = gen(H)
+    q = torch.randn(B, 1, H, D, generator=g, device="cuda").to(torch.bfloat16)
+    swa = C.SwaCache.of(e4m3_rows(g, B, max(1, window), D), scale=0.5, window=window) if window else None
+    wide = C.SwaCache.of(e4m3_rows(g, B, 520, D), scale=0.5, window=500)
+    pos = i32([[lens[b % 20] + 9] for b in range(B)])
+    outs = []
+    for power in (20, -30, 20):
+        x = (q.float() * 2.0 ** power).to(torch.bfloat16)
+        for _ in range(3):
+            a, b = torch.full_like(q, 7), torch.full_like(q, 7)
+            C.csa2_prefix_attn_decode(pool, many, 150, swa, x, pos, 0.0625 * 2.0 ** -power, a)
+            C.csa2_window_attn(wide, None, x, pos, 0.0625 * 2.0 ** -power, b)
+            outs.append((a, b))
+    assert all(torch.equal(a, outs[0][0]) and torch.equal(b, outs[0][1]) for a, b in outs)
+    assert C.csa2_device_status() == 0
+
+
+# --------------------------------------------------------------------------- planes of more than 4 GB
+
+
+def test_pages_behind_four_gigabytes():
+    """Append, attention, fork and compact where a page's bytes lie beyond 32 bits."""
+    D, page, n_pages, n = 512, 128, 140_000, 300
+    pool = C.PagePool(n_pages, page, 3, 4, D)
+    assert pool.codes.numel() > 2 ** 32
+    pool.refs[: n_pages - 8] = 1                          # only the last eight pages are free
+    g = gen(9)
+    src = C.MainCache(1, 384, D, 64, 1)
+    src.codes.copy_(torch.randint(0, 256, src.codes.shape, generator=g, device="cuda", dtype=torch.uint8))
+    src.scales.copy_(torch.randint(0x20, 0x38, src.scales.shape, generator=g, device="cuda", dtype=torch.uint8))
+    src.n_entries.copy_(i32([n]))
+    C.csa2_pages_append(pool, src, i32([0]))
+    C.csa2_pages_fork(pool, i32([0]), i32([1]))
+    C.csa2_pages_append(pool, src, i32([1]), at=i32([200]), first=i32([250]))       # copies the second page's start
+    assert pool.table[0, :3].tolist() == [n_pages - 8, n_pages - 7, n_pages - 6]
+    assert pool.table[1, :2].tolist() == [n_pages - 8, n_pages - 5]
+    from test_gpu_paged import fp4_values
+    v0 = fp4_values(src.codes[0, :n], src.scales[0, :n])
+    v1 = torch.cat([v0[:200], v0[250:300]])
+    q = torch.randn(2, 1, 64, D, generator=g, device="cuda").to(torch.bfloat16)
+    out = torch.empty_like(q)
+
+    def attend(what):
+        out.fill_(7)
+        C.csa2_prefix_attn_decode(pool, i32([0, 1]), 200, None, q, i32([[n], [n]]), 0.044, out)
+        for b, v in enumerate((v0, v1)):
+            check(out[b, 0], *attend64(q[b, 0].double(), v, 0.044), f"{what}, b {b}")
+
+    attend("far")
+    pool.refs[: n_pages - 8] = 0
+    live = torch.zeros(1, dtype=torch.int32, device="cuda")
+    C.csa2_pages_compact(pool, live)
+    assert int(live) == 4 and int(pool.table.max()) == 3
+    attend("near")
+    assert C.csa2_device_status() == 0
+
+
+@pytest.mark.parametrize("window", [128, 600])
+def test_window_rows_behind_four_gigabytes(window):
+    B, W_cap, D, H = 4, 2_200_000, 512, 16
+    rows = torch.zeros(B, W_cap, D, dtype=torch.uint8, device="cuda")
+    assert rows.numel() > 2 ** 32
+    g = gen(3)
+    pos = [[1500], [W_cap - 1], [W_cap + 5], [2 * W_cap + 2_100_000]]
+    for b in range(B):
+        at = torch.arange(pos[b][0] - window + 1, pos[b][0] + 1, device="cuda") % W_cap
+        rows[b, at] = e4m3_rows(g, window, D)
+    q = torch.randn(B, 1, H, D, generator=g, device="cuda").to(torch.bfloat16)
+    out = torch.empty_like(q)
+    C.csa2_window_attn(C.SwaCache.of(rows, scale=0.5, window=window), None, q, i32(pos), 0.05, out)
+    for b in range(B):
+        check(out[b, 0], *attend64(q[b, 0].double(), window_keys(rows[b], 0.5, pos[b][0], window), 0.05), f"b {b}")
+    assert C.csa2_device_status() == 0
