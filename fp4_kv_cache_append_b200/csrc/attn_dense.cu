@@ -20,10 +20,10 @@
 //               warps take the groups in turn.  The chunks that only S needs
 //               come first and are freed first
 //   warps 8-11  softmax, one row per thread: no exchange between threads.  The
-//               reference maximum moves only when a weight exceeds its by 2^6.9;
-//               O is then rescaled in tensor memory.  P, 2^9 times the weight
-//               against the reference, goes back to tensor memory (fp16) as the
-//               A operand of the second product
+//               reference, 2^9 below the maximum, moves only when a weight
+//               passes 2^15.9 against it; O is then rescaled in tensor memory.  P
+//               goes back to tensor memory (fp16) as the A operand of the second
+//               product
 //   warps 12, 14  tcgen05.mma issuers of S and of O, one lane each: S of tile
 //               i + 1 runs during tile i's softmax, O of tile i as soon as its P
 //               is there
@@ -104,9 +104,10 @@ constexpr int kRawRow = 128, kRawSc = kTile * kRawRow, kRawBytes = kRawSc + kTil
 // above takes 427 us with 2, 363 with 5, 343 with 8, 345 with 10 and 349 with 16.
 // (At D 128 and 256, where a tile takes less, it was not fitted.)
 constexpr int kUnitCost = 8;
-// P = 2^(x - reference + kBias), at most 2^(kBias + kLazy) = 61,147, below fp16's
-// 65,504.  The row's largest weight is then at least 2^9, weights down to 2^-23
-// of it keep fp16's 11 bits and none above 2^-34 of it becomes 0, while the
+// P = 2^(x - reference), where the reference is set kBias below the largest x so
+// far once P would pass 2^(kBias + kLazy) = 61,147 (fp16 ends at 65,504).  The
+// row's largest weight is then at least 2^9, weights down to 2^-23 of it keep
+// fp16's 11 bits and none above 2^-34 of it becomes 0, while the
 // denominator sums all of them in fp32: n keys lose at most n 2^-34 of the row's
 // weight.  (Without the bias n 2^-25: one key 17 nats above a million equal ones
 // took 3% from the output.)  A lower limit moves the reference more often: a
@@ -927,17 +928,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_dense_kernel(const __grid_co
           for (int u = 0; u < 4; ++u)
             mx4[u] = j + 4 + u < kTile ? fmaxf(mx4[u], fmaxf(__uint_as_float(sv[j + u]), __uint_as_float(sv[j + 4 + u])))
                                        : fmaxf(mx4[u], __uint_as_float(sv[j + u]));
-        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * lsc;
+        // The largest exponent against the reference, by the operation that forms the
+        // exponents, so that the rounding of a large logit does not take P out of
+        // fp16's range.  The reference may be rounded, up: it is what all are relative
+        // to, and the largest weight is 2^9 less a step of the logits' fp32 at least
+        // (2^-7 up to 2^28, where a step is 16).  Without a reference yet the exponent
+        // is +inf, or NaN if nothing is seen.
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         float al = 1.f;
-        if (mx > m_ref + kLazy || (m_ref == -INFINITY && mx != -INFINITY)) {
-          al = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - mx);
-          m_ref = mx;
+        if (fmaf(mx, lsc, -m_ref) > kBias + kLazy) {
+          const float m_new = __fmaf_ru(mx, lsc, -kBias);
+          al = ex2_approx(m_ref - m_new);
+          m_ref = m_new;
           l *= al;
         }
         const float mu = m_ref == -INFINITY ? 0.f : m_ref;
         uint32_t pr[kTile / 2];
         {
-          const uint64_t l2 = f32x2(lsc, lsc), m2 = f32x2(kBias - mu, kBias - mu);
+          const uint64_t l2 = f32x2(lsc, lsc), m2 = f32x2(-mu, -mu);
           uint64_t ls0 = 0, ls1 = 0;
 #pragma unroll
           for (int j = 0; j < kTile / 2; ++j) {

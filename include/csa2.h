@@ -470,9 +470,10 @@ CSA2_API csa2_status csa2_pages_compact(const csa2_page_pool *pool, int32_t *n_l
  * The products run in fp16 with every row of q multiplied by a power of two: q
  * may be of any size, and rounding moves an element by 2^-23 of its row's
  * largest at most.
- * The logits have to be finite in FP32.  Weights are rounded to fp16 for the
- * second product, the largest of a row lying at 2^9 or above: n keys lose at
- * most n 2^-34 of a row's weight.
+ * Weights are rounded to fp16 for the second product, the largest of a row
+ * lying at 2^9 or above: n keys lose at most n 2^-34 of a row's weight.
+ * Logits may be up to 10^8 in magnitude (a row with larger ones stays finite
+ * but may lose its output).
  * Supported: 1 <= H <= 64, B * T_q <= 65,535, window <= 1024.
  */
 CSA2_API csa2_status csa2_prefix_attn_decode(const csa2_page_pool *pool, const int32_t *seq, int n_shared,

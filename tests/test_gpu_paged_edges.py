@@ -418,3 +418,35 @@ def test_window_rows_behind_four_gigabytes(window):
     for b in range(B):
         check(out[b, 0], *attend64(q[b, 0].double(), window_keys(rows[b], 0.5, pos[b][0], window), 0.05), f"b {b}")
     assert C.csa2_device_status() == 0
+
+
+# --------------------------------------------------------------------------- logits of millions
+
+
+@pytest.mark.parametrize("D,H,size", [(128, 8, 2e5), (256, 20, 1e6), (512, 64, 4e5), (128, 64, 3e6)])
+def test_logits_of_millions_stay_finite(D, H, size):
+    """A step of fp32 is then larger than the headroom of the weights in fp16: no
+    weight may leave fp16's range for it.  (One key takes all: attend64's tolerance
+    is wide, but finite.)"""
+    pool, seq, values = paged_batch(D + H, D, 16, 300, [700, 310, 433])
+    g = gen(H)
+    q = torch.randn(3, 4, H, D, generator=g, device="cuda").to(torch.bfloat16)
+    rows = e4m3_rows(g, 3, 1100, D)
+    pos = [[698 + j for j in range(4)], [305 + j for j in range(4)], [500 + j for j in range(4)]]
+    for scale in (size, -size):
+        for window, k in ((600, None), (100, None), (100, pool)):
+            swa = C.SwaCache.of(rows, scale=0.5, window=window)
+            out = torch.empty_like(q)
+            if k is None:
+                C.csa2_window_attn(swa, None, q, i32(pos), scale, out)
+            else:
+                C.csa2_prefix_attn_decode(k, seq, 300, swa, q, i32(pos), scale, out)
+            assert bool(torch.isfinite(out).all()), (scale, window)
+            for b in range(3):
+                for j in range(4):
+                    t = pos[b][j]
+                    keys = [window_keys(rows[b], 0.5, t, window)] + ([] if k is None else [values[b][: t + 1]])
+                    keys = torch.cat(keys)
+                    ref, tol = attend64(q[b, j].double(), keys, scale)
+                    check(out[b, j], ref, tol, f"scale {scale} window {window} b {b} query {j}")
+    assert C.csa2_device_status() == 0
