@@ -450,3 +450,130 @@ def test_logits_of_millions_stay_finite(D, H, size):
                     ref, tol = attend64(q[b, j].double(), keys, scale)
                     check(out[b, j], ref, tol, f"scale {scale} window {window} b {b} query {j}")
     assert C.csa2_device_status() == 0
+
+
+# --------------------------------------------------------------------------- the largest lists, batches and positions
+
+
+def test_lists_of_the_largest_length():
+    n, page, D = 4096, 16, 128
+    g, rng = gen(4), np.random.default_rng(4)
+    pool = C.PagePool(9000, page, n + 5, 3, D)
+    ref = Model(pool)
+    src = C.MainCache(n, 128, D, 64, 1)
+    src.codes.copy_(torch.randint(0, 256, src.codes.shape, generator=g, device="cuda", dtype=torch.uint8))
+    src.scales.copy_(torch.randint(0, 256, src.scales.shape, generator=g, device="cuda", dtype=torch.uint8))
+    src.n_entries.copy_(i32(rng.integers(0, 40, n)))
+    host = (src.codes.cpu().numpy(), src.scales.cpu().numpy(), src.n_entries.cpu().numpy())
+    ws = C.workspace(C.csa2_pages_workspace_size(pool, n))
+    for _ in range(2):
+        seq = rng.permutation(n + 5)[:n].astype(np.int32)
+        seq[[5, 4000]], seq[77] = seq[9], -1
+        C.csa2_pages_append(pool, src, i32(seq), ws=ws)
+        ref.append(*host, seq)
+        ref.same(pool, "append")
+        parent, child = rng.integers(-1, n + 5, n), rng.permutation(n + 5)[:n]
+        child[[100, 4095]] = child[3]
+        C.csa2_pages_fork(pool, i32(parent), i32(child), ws=ws)
+        ref.fork(parent.tolist(), child.tolist())
+        ref.same(pool, "fork")
+    C.csa2_pages_compact(pool, ws=ws)
+    ref.compact()
+    ref.same(pool, "compact")
+    assert C.csa2_device_status() == (C.DEV_BAD_SEQUENCE | C.DEV_NO_PAGE if ref.no_page else C.DEV_BAD_SEQUENCE)
+
+
+@pytest.mark.parametrize("B,T,n_shared,window", [(65535, 1, 0, 0), (65535, 1, 50, 3), (1, 65535, 100, 0), (255, 257, 70, 2)])
+def test_prefix_attention_of_the_most_queries(B, T, n_shared, window):
+    D, H = 128, 1
+    lens = [n_shared + 5 + 7 * i for i in range(12)]
+    pool, seq, values = paged_batch(B % 97, D, 16, n_shared, lens)
+    pick = torch.arange(B, device="cuda") * 5 % 12
+    g = gen(B)
+    q = torch.randn(B, T, H, D, generator=g, device="cuda").to(torch.bfloat16)
+    rows = e4m3_rows(g, B, window + T - 1, D) if window else None
+    swa = C.SwaCache.of(rows, scale=0.5, window=window) if window else None
+    pos = (torch.arange(B, device="cuda")[:, None] % 40 + torch.arange(T, device="cuda")[None]).to(torch.int32)
+    buf, out = guarded((B, T, H, D))
+    C.csa2_prefix_attn_decode(pool, seq[pick].contiguous(), n_shared, swa, q, pos, 0.09, out)
+    assert bool((buf[:1024] == 7).all()) and bool((buf[-1024:] == 7).all())
+    rng = np.random.default_rng(B)
+    for b, j in [(0, 0), (B - 1, T - 1)] + [(int(rng.integers(B)), int(rng.integers(T))) for _ in range(60)]:
+        t, i = int(pos[b, j]), int(pick[b])
+        keys = [values[i][: min(lens[i], t + 1)]]
+        if window:
+            keys.append(window_keys(rows[b], 0.5, t, window))
+        check(out[b, j], *attend64(q[b, j].double(), torch.cat(keys), 0.09), f"b {b} query {j}")
+    assert C.csa2_device_status() == 0
+
+
+@pytest.mark.parametrize("B,T,H", [(1, 1 << 22, 1), (1 << 22, 1, 1), (2048, 2048, 1)])
+def test_window_attention_of_the_most_queries(B, T, H):
+    D, W = 128, 3
+    g = gen(T)
+    rows = torch.randint(0x20, 0x48, (B, W + T - 1, D), generator=g, device="cuda", dtype=torch.uint8)
+    q = torch.randn(B, T, H, D, generator=g, device="cuda", dtype=torch.bfloat16)
+    pos = (torch.arange(B, device="cuda")[:, None] % 50 + torch.arange(T, device="cuda")[None]).to(torch.int32)
+    out = torch.empty_like(q)
+    C.csa2_window_attn(C.SwaCache.of(rows, scale=0.5, window=W), None, q, pos, 0.09, out)
+    rng = np.random.default_rng(T)
+    for b, j in [(0, 0), (B - 1, T - 1)] + [(int(rng.integers(B)), int(rng.integers(T))) for _ in range(60)]:
+        check(out[b, j], *attend64(q[b, j].double(), window_keys(rows[b], 0.5, int(pos[b, j]), W), 0.09), f"b {b} query {j}")
+    assert C.csa2_device_status() == 0
+
+
+@pytest.mark.parametrize("D,H,window,n_sink", [(128, 8, 100, 3), (512, 64, 100, 0), (256, 20, 700, 5), (512, 16, 1024, 2)])
+def test_the_largest_positions(D, H, window, n_sink):
+    """2^31 - 4,097 is the last position that is taken; those above count as padded queries."""
+    last, T = 2 ** 31 - 4097, 3
+    g = gen(D)
+    rows = e4m3_rows(g, 2, window + 17, D)
+    sink_rows = e4m3_rows(g, 2, max(1, n_sink), D)
+    swa = C.SwaCache.of(rows, scale=0.5, window=window)
+    sinks = C.SwaCache.of(sink_rows, scale=0.5, window=n_sink) if n_sink else None
+    pool, seq, values = paged_batch(D, D, 16, 40, [50, 90])
+    q = torch.randn(2, T, H, D, generator=g, device="cuda").to(torch.bfloat16)
+    for pos, flags in (([[last - 2, last - 1, last], [last - 9, last, last - 5]], 0),
+                       ([[last, last + 1, 2 ** 31 - 1], [last + 1, last - 1, last + 4096]], C.DEV_BAD_POSITION)):
+        for paged in (False, True):
+            out = torch.full_like(q, 7)
+            if paged:
+                C.csa2_prefix_attn_decode(pool, seq, 40, swa, q, i32(pos), 0.06, out)
+            else:
+                C.csa2_window_attn(swa, sinks, q, i32(pos), 0.06, out)
+            for b in range(2):
+                for j in range(T):
+                    t = pos[b][j]
+                    if t > last:
+                        assert bool((out[b, j] == 0).all())
+                        continue
+                    keys = [window_keys(rows[b], 0.5, t, window)]
+                    if paged:
+                        keys.append(values[b])
+                    elif n_sink:
+                        keys.append(sink_rows[b, :n_sink].view(torch.float8_e4m3fn).double() * 0.5)
+                    check(out[b, j], *attend64(q[b, j].double(), torch.cat(keys), 0.06), f"paged {paged} b {b} query {j}")
+            assert C.csa2_device_status() == flags
+
+
+@pytest.mark.parametrize("D,H,window", [(128, 8, 100), (512, 64, 100), (256, 20, 700), (512, 16, 1024)])
+def test_padded_queries_may_hold_anything(D, H, window):
+    """NaN and infinities in the q of padded queries reach neither their own
+    outputs (zeros) nor a bit of the others'."""
+    g = gen(D + window)
+    B, T = 3, 4
+    pool, seq, _ = paged_batch(D, D, 16, 40, [50, 90, 61])
+    swa = C.SwaCache.of(e4m3_rows(g, B, window + T, D), scale=0.5, window=window)
+    q = torch.randn(B, T, H, D, generator=g, device="cuda").to(torch.bfloat16)
+    pos = i32([[70, -1, 71, 72], [-1, -1, -1, -1], [1500, 1501, -1, -1]])
+    dirty = q.clone()
+    dirty[pos < 0] = torch.tensor([math.nan, math.inf, -math.inf, 3e38], dtype=torch.bfloat16, device="cuda").repeat(D // 4)
+    outs = []
+    for x in (q, dirty):
+        a, b = torch.full_like(q, 7), torch.full_like(q, 7)
+        C.csa2_prefix_attn_decode(pool, seq, 40, swa, x, pos, 0.06, a)
+        C.csa2_window_attn(swa, None, x, pos, 0.06, b)
+        assert bool((a[pos < 0] == 0).all()) and bool((b[pos < 0] == 0).all())
+        outs.append((a, b))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    assert C.csa2_device_status() == 0
